@@ -240,6 +240,37 @@ METIS_API int metis_moe_fp8_grouped_gemm_noalloc(const void* x_bf16, const int32
                                                  const uint8_t* w_down, const float* s_down,
                                                  int act, void* y_bf16, metis_stream_t stream);
 
+/* Routed-expert layer in the default maths, for few tokens: the FP8 weights
+ * are widened exactly to 16 bits as they are multiplied, and nothing else is
+ * quantized ("Lernex/Metis-1.6-Logos-FP8", "What --fast-math does": one
+ * conversation always decodes with the default maths, and several do without
+ * fast-math). Each chosen expert's weights are read once from HBM, whatever
+ * the number of its tokens:
+ *   h[t, j] = s_up[e]   * sum_k x[t, k]    D(w_up[e][., k]),  e = topk_ids[t, j]
+ *   o[t, j] = s_down[e] * sum_i h[t, j, i] D(w_down[e][., i])
+ *   y[t]    = bf16_rn( sum_j topk_w[t, j] o[t, j] ),
+ * products of 16-bit values with FP32 sums. x keeps its BF16 values (elements
+ * below 2^-29 of the token's largest magnitude lose bits, and below 2^-39 of
+ * it count as zero); h is held in FP32 and rounded to 11 significant bits
+ * (FP16 after a power-of-two shift of its row) where it is multiplied.
+ *   x [T, H] BF16, topk_ids [T, topk] int32 in [0, E), topk_w [T, topk] FP32,
+ *   w_up [E, I, H] E4M3, s_up [E, I], w_down [E, H, I] E4M3, s_down [E, H],
+ *   y [T, H] BF16 out. act must be METIS_ACT_NONE.
+ *   An id outside [0, E) drops its slot, as in metis_moe_fp8_grouped_gemm (the
+ *   sticky device error word records it); a token without any expert gets
+ *   zeros. The same expert may be named twice by a token. A token whose x
+ *   holds an infinity or a NaN gets a non-finite output; others are unaffected.
+ *   Requires H and I multiples of 16 in [16, 8192], 1 <= topk <= E <= 1024,
+ *   0 <= T <= 128 and T * topk <= 1024 (METIS_ERR_UNSUPPORTED beyond: the
+ *   grouped GEMM layer is made for more); x, weights and y 16-byte aligned.
+ *   Needs `workspace` of metis_workspace_size(METIS_OP_MOE_W8A16, T, I, H,
+ *   topk, E) bytes (256-byte aligned), overwritten: calls that may overlap on
+ *   the GPU need one each. */
+METIS_API int metis_moe_w8a16(const void* x_bf16, const int32_t* topk_ids, const float* topk_w, int64_t T,
+                              int64_t topk, int64_t E, int64_t H, int64_t I, const uint8_t* w_up,
+                              const float* s_up, const uint8_t* w_down, const float* s_down, int act,
+                              void* y_bf16, void* workspace, size_t ws_bytes, metis_stream_t stream);
+
 /* BF16 GEMM on the tensor cores (tcgen05.mma kind::f16, FP32 accumulation):
  *   y[m, n] = bf16_rn( sum_k x[m, k] w[n, k] ).
  * The shared expert's projections use it ("Lernex/Metis-1.6-Praxis" card,
@@ -287,6 +318,7 @@ METIS_API int metis_moe_shared_fused_combine(const void* x_bf16, int64_t T, int6
 #define METIS_OP_LINEAR 4
 #define METIS_OP_SHARED 6       /* metis_moe_shared_fused_combine: (T, I_s, H, topk, 0) */
 #define METIS_OP_W8A16_WIDENED 7 /* metis_w8a16_gemm_widened: 2 * N * K bytes */
+#define METIS_OP_MOE_W8A16 8    /* metis_moe_w8a16: (T, I, H, topk, E) */
 METIS_API size_t metis_workspace_size(int op, int64_t M_or_T, int64_t N_or_I, int64_t K_or_H,
                             int64_t topk, int64_t E);
 

@@ -57,6 +57,8 @@ extern "C" {
 #define METIS_SF_ROWMAJOR 0    /* block scales [R, K/16] */
 #define METIS_SF_TILED 1       /* block scales in the tensor-core atom layout */
 #define METIS_OP_MOE_NVFP4 5   /* metis_workspace_size: the NVFP4 routed-expert layer */
+#define METIS_OP_MOE_NVFP4_W4A16 9 /* metis_moe_nvfp4_w4a16: (T, I, H, topk, E) */
+#define METIS_OP_NVFP4_W4A16 10    /* metis_nvfp4_w4a16_gemm: (M, N, K) */
 
 /*
  * NVFP4 quantization of R rows of K elements (the reading above).
@@ -148,6 +150,41 @@ METIS_API int metis_moe_nvfp4_grouped_gemm(const void* x_bf16, const int32_t* to
 /* Byte offset of a region in the workspace, or -1 for a bad argument. */
 METIS_API int64_t metis_moe_nvfp4_workspace_offset(int region, int64_t T, int64_t topk, int64_t E,
                                                    int64_t H, int64_t I);
+
+/*
+ * Routed-expert layer with NVFP4 experts in the default maths, for few tokens
+ * ("Lernex/Metis-1.6-Praxis-NVFP4", "What --fast-math does": one stream's
+ * decode always uses the default maths, in which the weights are the only
+ * thing rounded). The steps, limits and behaviour of metis_moe_w8a16, with
+ *   W[e] = g[e] * D2(q) * D(sf),
+ * each weight D2(q) * D(sf) widened exactly to 16 bits.
+ *   Arrays as in metis_moe_nvfp4_grouped_gemm (tiled scales), so that one set
+ *   of weights serves both layers; y is required.
+ *   Requires H and I multiples of 128 in [128, 8192], 1 <= topk <= E <= 1024,
+ *   0 <= T <= 128, T * topk <= 1024; x, codes, tiled scales and y 16-byte aligned.
+ *   workspace  metis_workspace_size(METIS_OP_MOE_NVFP4_W4A16, T, I, H, topk, E)
+ *              bytes, 256-byte aligned.
+ */
+METIS_API int metis_moe_nvfp4_w4a16(const void* x_bf16, const int32_t* topk_ids, const float* topk_w,
+                                    int64_t T, int64_t topk, int64_t E, int64_t H, int64_t I,
+                                    const uint8_t* w_up, const uint8_t* sf_up, const float* g_up,
+                                    const uint8_t* w_down, const uint8_t* sf_down, const float* g_down,
+                                    int act, void* y_bf16, void* workspace, size_t ws_bytes,
+                                    metis_stream_t stream);
+
+/*
+ * Default-maths product with NVFP4 weights:
+ *   y [M, N] = bf16_rn( g_b * sum_k x[m, k] D2(qb[n, k]) D(sfb[n, k/16]) ),
+ * x BF16, the weights widened exactly to 16 bits, FP32 sums.
+ *   x [M, K] BF16 (dense rows); qb, sfb, gb as in metis_nvfp4_gemm.
+ * K a multiple of 64 in [64, 65536], N a multiple of 128 up to 2^20, M >= 0;
+ * x, codes, tiled scales and y 16-byte aligned.
+ *   workspace  metis_workspace_size(METIS_OP_NVFP4_W4A16, M, N, K, 0, 0)
+ *              bytes, 256-byte aligned; 0 (NULL allowed) for few tokens.
+ */
+METIS_API int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, const uint8_t* sfb,
+                                     const float* gb, void* y_bf16, int64_t M, int64_t N, int64_t K,
+                                     void* workspace, size_t ws_bytes, metis_stream_t stream);
 
 #ifdef __cplusplus
 }

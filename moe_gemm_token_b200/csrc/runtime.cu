@@ -280,6 +280,9 @@ int64_t moe4_region_offset(int region, int64_t T, int64_t topk, int64_t E, int64
     return at;
 }
 
+// few_tokens.cu
+size_t few_moe_workspace(int64_t T, int64_t topk, int64_t H, int64_t I);
+
 }  // namespace metis
 
 using namespace metis;
@@ -370,6 +373,10 @@ extern "C" size_t metis_workspace_size(int op, int64_t M_or_T, int64_t N_or_I, i
             moe4_region_offset(0, M_or_T, topk, E, K_or_H, N_or_I, &total);
             return static_cast<size_t>(total);
         }
+        case METIS_OP_MOE_W8A16:
+        case METIS_OP_MOE_NVFP4_W4A16:
+            if (topk < 1 || E < 1) return 0;
+            return few_moe_workspace(M_or_T, topk, K_or_H, N_or_I);
         default:
             return 0;
     }

@@ -1,4 +1,5 @@
-"""Thin Python binding of libmetis_fp8 (the C ABI in ``include/metis_fp8.h``).
+"""Thin Python binding of libmetis_fp8 (the C ABI in ``include/metis_fp8.h``,
+``include/metis_nvfp4.h`` and ``include/metis_mxfp4.h``).
 
 Every function here has the name of the C entry point it calls and only
 marshals arguments: torch CUDA tensors become device pointers, shapes become
@@ -34,6 +35,9 @@ METIS_OP_LINEAR = 4
 METIS_OP_MOE_NVFP4 = 5
 METIS_OP_SHARED = 6
 METIS_OP_W8A16_WIDENED = 7
+METIS_OP_MOE_W8A16 = 8
+METIS_OP_MOE_NVFP4_W4A16 = 9
+METIS_OP_NVFP4_W4A16 = 10
 METIS_A_F32 = 2
 METIS_SF_ROWMAJOR = 0
 METIS_SF_TILED = 1
@@ -89,6 +93,13 @@ def load():
         "metis_moe_nvfp4_grouped_gemm": ([p, p, p, i64, i64, i64, i64, i64, p, p, p, p, p, p, i32,
                                           p, p, sz, p], i32),
         "metis_moe_nvfp4_workspace_offset": ([i32, i64, i64, i64, i64, i64], i64),
+        "metis_moe_w8a16": ([p, p, p, i64, i64, i64, i64, i64, p, p, p, p, i32, p, p, sz, p], i32),
+        "metis_moe_nvfp4_w4a16": ([p, p, p, i64, i64, i64, i64, i64, p, p, p, p, p, p, i32, p, p, sz,
+                                   p], i32),
+        "metis_nvfp4_w4a16_gemm": ([p, p, p, p, p, i64, i64, i64, p, sz, p], i32),
+        "metis_quant_mxfp4": ([p, i32, i64, i64, i64, p, p, i32, p], i32),
+        "metis_dequant_mxfp4": ([p, p, i32, i64, i64, p, p], i32),
+        "metis_mxfp4_gemm": ([p, p, p, p, p, i64, i64, i64, p], i32),
         "metis_bf16_gemm": ([p, p, p, i64, i64, i64, p], i32),
         "metis_moe_shared_fused_combine": ([p, i64, i64, i64, p, p, p, p, p, i64, p, p, sz, p], i32),
     }
@@ -120,6 +131,26 @@ def _check(name, rc):
     if rc != METIS_OK:
         raise MetisError(name, rc, load().metis_last_error().decode())
     return rc
+
+
+def _dense(name, *tensors):
+    """The tensors' checks that the C entry point cannot make: CUDA tensors of
+    one device, the current one, with dense rows."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if not t.is_cuda or t.device.index != device:
+            raise ValueError(f"{name}: tensors must be on the current CUDA device ({device}), got {t.device}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: tensors must be contiguous")
+
+
+def _need(name, ok, what):
+    if not ok:
+        raise ValueError(f"{name}: {what}")
+
+
+def _bytes(workspace):
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def _rows(t):
@@ -290,6 +321,113 @@ def metis_moe_nvfp4_workspace_offset(region, T, topk, E, H, I):
         region = MOE4_WS[region]
     return int(load().metis_moe_nvfp4_workspace_offset(int(region), int(T), int(topk), int(E),
                                                        int(H), int(I)))
+
+
+# ------------------------------------------- default maths for few tokens
+
+def _moe_few(name, x, topk_ids, topk_w, up, down, codes_per_byte, y, workspace, act, stream):
+    """The two few-token routed layers: shape checks and the call; `up` and
+    `down` are (weights, scales...) as the C entry point takes them."""
+    T, H = x.shape
+    topk = topk_ids.shape[1]
+    E, I, hb = up[0].shape
+    _need(name, x.dtype == torch.bfloat16 and y.dtype == torch.bfloat16, "x and y must be torch.bfloat16")
+    _need(name, topk_ids.dtype == torch.int32 and topk_w.dtype == torch.float32,
+          "topk_ids must be torch.int32 and topk_w torch.float32")
+    _need(name, topk_ids.shape == (T, topk) and topk_w.shape == (T, topk) and y.shape == (T, H),
+          "topk_ids, topk_w and y must match x")
+    _need(name, hb * codes_per_byte == H and down[0].shape == (E, H, I // codes_per_byte),
+          "w_up must be [E, I, H] and w_down [E, H, I]")
+    _dense(name, x, topk_ids, topk_w, *up, *down, y, workspace)
+    return _check(name, getattr(load(), name)(
+        _p(x), _p(topk_ids), _p(topk_w), T, topk, E, H, I, *map(_p, up), *map(_p, down), int(act), _p(y),
+        _p(workspace), _bytes(workspace), _s(stream)))
+
+
+def metis_moe_w8a16(x, topk_ids, topk_w, w_up, s_up, w_down, s_down, y, workspace, act=METIS_ACT_NONE,
+                    stream=None):
+    """Routed-expert layer in the default maths (FP8 weights, BF16 activations)
+    for few tokens; see the C header for shapes."""
+    name = "metis_moe_w8a16"
+    _need(name, s_up.shape == w_up.shape[:2] and s_down.shape == w_down.shape[:2] and
+          s_up.dtype == s_down.dtype == torch.float32, "s_up must be FP32 [E, I] and s_down FP32 [E, H]")
+    return _moe_few(name, x, topk_ids, topk_w, (w_up, s_up), (w_down, s_down), 1, y, workspace, act, stream)
+
+
+def metis_moe_nvfp4_w4a16(x, topk_ids, topk_w, w_up, sf_up, g_up, w_down, sf_down, g_down, y, workspace,
+                          act=METIS_ACT_NONE, stream=None):
+    """Routed-expert layer in the default maths with NVFP4 experts, for few
+    tokens; weights and tiled scales as in :func:`metis_moe_nvfp4_grouped_gemm`."""
+    name = "metis_moe_nvfp4_w4a16"
+    E, I, hb = w_up.shape
+    _need(name, sf_up.numel() * 8 == w_up.numel() and sf_down.numel() * 8 == w_down.numel(),
+          "sf_up and sf_down must hold one byte per 16 elements")
+    _need(name, g_up.numel() == E and g_down.numel() == E and g_up.dtype == g_down.dtype == torch.float32,
+          "g_up and g_down must be FP32 [E]")
+    return _moe_few(name, x, topk_ids, topk_w, (w_up, sf_up, g_up), (w_down, sf_down, g_down), 2, y, workspace,
+                    act, stream)
+
+
+def metis_nvfp4_w4a16_gemm(x, qb, sfb, gb, y, workspace=None, stream=None):
+    """y [M, N] = x [M, K] times NVFP4 weights (codes [N, K/2], tiled scales, one
+    FP32 global scale on the device) in the default maths."""
+    name = "metis_nvfp4_w4a16_gemm"
+    M, K = x.shape
+    N = qb.shape[0]
+    _need(name, x.dtype == torch.bfloat16 and y.dtype == torch.bfloat16, "x and y must be torch.bfloat16")
+    _need(name, qb.shape == (N, K // 2) and y.shape == (M, N) and sfb.numel() * 16 >= (N + 127) // 128 * 128 * K,
+          "qb must be [N, K/2], sfb its tiled scales and y [M, N]")
+    _need(name, gb.numel() == 1 and gb.dtype == torch.float32, "gb must be one FP32 value")
+    _dense(name, x, qb, sfb, gb, y, *(() if workspace is None else (workspace,)))
+    return _check(name, load().metis_nvfp4_w4a16_gemm(
+        _p(x), _p(qb), _p(sfb), _p(gb), _p(y), M, N, K, _p(workspace), _bytes(workspace), _s(stream)))
+
+
+# ------------------------------------------------------------------ MXFP4
+
+def metis_quant_mxfp4(x, q, sf, tiled=False, stream=None):
+    """x [R, K] BF16 or FP32 -> q [R, K/2] packed E2M1 codes and sf E8M0 scales
+    per 32 elements (row-major [R, K/32], or tiled). Rows of x may be strided."""
+    name = "metis_quant_mxfp4"
+    R, K, ldx = _rows(x)
+    _need(name, x.dtype in (torch.bfloat16, torch.float32), "x must be torch.bfloat16 or torch.float32")
+    _need(name, x.stride(1) == 1 or K == 1, "the rows of x must be contiguous")
+    rows = (R + 127) // 128 * 128 if tiled else R
+    _need(name, q.numel() * 2 >= R * K and sf.numel() * 32 >= rows * K, "q or sf is too small")
+    _need(name, x.is_cuda and x.device == q.device, "tensors must be on one CUDA device")
+    _dense(name, q, sf)
+    kind = METIS_A_F32 if x.dtype == torch.float32 else METIS_A_BF16
+    return _check(name, load().metis_quant_mxfp4(
+        _p(x), kind, R, K, ldx if R > 1 else K, _p(q), _p(sf), METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR,
+        _s(stream)))
+
+
+def metis_dequant_mxfp4(q, sf, y, tiled=False, stream=None):
+    """The values of MXFP4 codes and scales as BF16 y [R, K]."""
+    name = "metis_dequant_mxfp4"
+    R, K = y.shape
+    rows = (R + 127) // 128 * 128 if tiled else R
+    _need(name, y.dtype == torch.bfloat16, "y must be torch.bfloat16")
+    _need(name, q.numel() * 2 >= R * K and sf.numel() * 32 >= rows * K, "q or sf is too small")
+    _dense(name, q, sf, y)
+    return _check(name, load().metis_dequant_mxfp4(
+        _p(q), _p(sf), METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR, R, K, _p(y), _s(stream)))
+
+
+def metis_mxfp4_gemm(qa, sfa, qb, sfb, y, stream=None):
+    """y [M, N] = product of two MXFP4 matrices (codes and tiled scales); qa
+    holds ceil(M/128)*128 rows."""
+    name = "metis_mxfp4_gemm"
+    M, N = y.shape
+    K = qb.shape[1] * 2
+    rows = (M + 127) // 128 * 128
+    _need(name, y.dtype == torch.bfloat16, "y must be torch.bfloat16")
+    _need(name, qb.shape[0] == N and qa.shape[1] * 2 == K and qa.shape[0] >= rows,
+          "qa must be [ceil(M/128) * 128, K/2] and qb [N, K/2]")
+    _need(name, sfa.numel() * 32 >= rows * K and sfb.numel() * 32 >= (N + 127) // 128 * 128 * K,
+          "sfa or sfb is too small")
+    _dense(name, qa, sfa, qb, sfb, y)
+    return _check(name, load().metis_mxfp4_gemm(_p(qa), _p(sfa), _p(qb), _p(sfb), _p(y), M, N, K, _s(stream)))
 
 
 # ------------------------------------------------------------ shared expert
