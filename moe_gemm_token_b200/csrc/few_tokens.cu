@@ -26,9 +26,15 @@ struct Weights {
     int N, K;
 };
 
-constexpr int WARPS = 8;
-constexpr int THREADS = WARPS * 32;
-constexpr int DEPTH = 6;         // pieces in flight per warp
+// Geometry by warps per CTA: 8 warps leave room on an SM for a CTA of the next
+// kernel, whose prologue then overlaps (few weights per SM: latency); 16 take
+// an SM by themselves and share one staged operand (many weights per SM).
+// depth: pieces in flight per warp. 64 KB per SM cover the memory latency.
+template <int W>
+struct Cta {
+    static constexpr int THREADS = W * 32;
+    static constexpr int DEPTH = W == 8 ? 8 : 4;
+};
 
 enum Mode { UP = 0, DOWN = 1, OWN = 2, DENSE = 3 };
 
@@ -38,7 +44,10 @@ template <int FMT>
 struct Geo {
     static constexpr int EL = FMT == FP8 ? 64 : 128;     // elements of K per piece
     static constexpr int CH = EL / 32;                   // 8-element chunks of K per lane
-    static constexpr int SLOT = 1024 + (FMT == FP8 ? 0 : 256);  // bytes of a piece in the ring
+    // a piece in the ring: codes [2][32][16]; then 4-byte words per lane: FP8
+    // the channel scales of its two rows, NVFP4 their block scales and the
+    // global scale
+    static constexpr int SLOT = 1024 + (FMT == FP8 ? 256 : 384);
 };
 
 struct Args {
@@ -47,36 +56,76 @@ struct Args {
     const int32_t* ids;    // [S]; DENSE: null
     const float* tw;       // OWN: [S] routing weights
     int E, S, T, topk;     // DENSE: E = 1, S = T = tokens
-    int P;                 // rows of the operand staged at a time
+    int P;                 // operand rows that are staged at a time, at most
+    int by_token;          // UP: all tokens are staged, before the routing is known
+    uint32_t grid_inv, tiles_inv;  // floor((2^32 - 1) / d) of the grid and of the tiles of a job
     int pitch;             // bytes between staged rows: 64 mod 128
     void* out;             // UP, DOWN: FP32 [S, N]; OWN: BF16 [T, N]; DENSE: BF16 [T, N]
     uint32_t* status;
 };
 
-// Shared memory: ring | partial sums | staged operand | its scales | routing.
-struct Smem {
-    int part, x, unshift, route, own, total;
+// A tile of 16 rows against the columns of one pass, as the threads that add
+// the warps' sums see it.
+struct Item {
+    int slot0, n, p, pe;   // first entry in the slot list, columns, first place, end of the places
 };
+
+// Bytes between staged operand rows: whole pieces, and 64 mod 128 so that the
+// lanes of two rows read different banks.
+template <int FMT>
+constexpr int operand_pitch(int K) {
+    return (K + Geo<FMT>::EL - 1) / Geo<FMT>::EL * Geo<FMT>::EL * 2 + 64;
+}
+
+// n / d and the rest, with inv = floor((2^32 - 1) / d): the product is at most one short.
+__device__ __forceinline__ int divide(uint32_t n, uint32_t d, uint32_t inv, int& rest) {
+    uint32_t q = __umulhi(n, inv), r = n - q * d;
+    if (r >= d) ++q, r -= d;
+    rest = static_cast<int>(r);
+    return static_cast<int>(q);
+}
+
+// Shared memory: ring | partial sums | staged operand | its scales | items | routing | outputs.
+struct Smem {
+    int part, x, unshift, items, route, own, total;
+};
+template <int W>
 __host__ __device__ inline Smem smem_layout(int slot_bytes, int gmax, int P, int pitch, int E, int S, bool routed,
                                             bool own) {
     Smem s;
-    s.part = WARPS * DEPTH * slot_bytes;
-    s.x = s.part + 2 * WARPS * 512 * gmax;
+    s.part = W * Cta<W>::DEPTH * slot_bytes;
+    s.x = s.part + (gmax == 1 ? 2 : 1) * W * 512 * gmax;
     s.unshift = s.x + P * pitch;
-    s.route = s.unshift + ((P * 4 + 15) & ~15);
-    s.own = s.route + (routed ? 4 * (E + 2 * (E < S ? E : S) + 2 + S) + 16 : 16);
+    s.items = s.unshift + ((P * 8 + 15) & ~15);
+    s.route = s.items + 2 * W * static_cast<int>(sizeof(Item));
+    s.own = s.route + (routed ? 4 * (E + 4 * S + 2) : 16);
     s.own = (s.own + 15) & ~15;
     s.total = s.own + (own ? S * 16 * 4 : 0);
     return s;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+// Asynchronous copies to shared memory; `zero`: the source is not read and
+// zeros are written.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool zero) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tcp.async.cg.shared.global [%0], [%1], 16, p;\n\t}" ::"r"(dst),
+                 "l"(src), "r"(static_cast<int>(zero)) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool valid) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, bool zero) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tcp.async.ca.shared.global [%0], [%1], 4, p;\n\t}" ::"r"(dst),
+                 "l"(src), "r"(static_cast<int>(zero)) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t p) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared4(uint32_t p) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(p) : "memory");
+    return v;
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int DEPTH>
 __device__ __forceinline__ void cp_async_wait_oldest() {
     asm volatile("cp.async.wait_group %0;" ::"n"(DEPTH - 1) : "memory");
 }
@@ -124,25 +173,10 @@ __device__ __forceinline__ int place_to_row(int p) {
     return FMT == FP8 ? p : (p & ~127) | ((p & 3) << 5) | ((p & 127) >> 2);
 }
 
-// Eight elements of an operand row as FP32.
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-    const uint4 a = *reinterpret_cast<const uint4*>(p);
-    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = bf16_lo(w[i]);
-        v[2 * i + 1] = bf16_hi(w[i]);
-    }
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-}
-
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// One warp stages one operand row [K] as FP16 after the power-of-two shift
-// that brings its largest magnitude into [2^14, 2^15) (exact for BF16 values
+// Operand rows [K] are staged as FP16 after the power-of-two shift that
+// brings a row's largest magnitude into [2^14, 2^15) (exact for BF16 values
 // within 2^-29 of the largest; FP32 values are rounded to 11 significant
 // bits). A row with an infinity or a NaN is not shifted. 16-byte chunks are
 // stored in the order in which the lanes read them (operand_chunk), zeros
@@ -153,126 +187,275 @@ __device__ __forceinline__ int operand_chunk(int q) {
     const int piece = q / (4 * C), r = q % (4 * C);
     return piece * 4 * C + (r % C) * 4 + r / C;
 }
-template <int FMT, typename In>
-__device__ __forceinline__ void stage_row(const In* row, int K, uint8_t* dst, float* unshift, int lane) {
-    const int chunks = K / 8;
-    uint32_t m = 0;
-    for (int q = lane; q < chunks; q += 32) {
-        float v[8];
-        load8(row + 8 * q, v);
+// Staging n operand rows by all warps: row i is src(i) and goes to dst + i *
+// pitch. W / n' warps share a row (n' = n rounded up to a power of two), so
+// that a few rows are read with one round trip, and a lane keeps its chunks
+// in registers between the two steps (largest magnitude, shift) when they fit.
+template <typename In>
+struct Chunk;  // eight elements as loaded
+template <>
+struct Chunk<__nv_bfloat16> {
+    uint4 w;
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
+    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-        for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    const int sh = m == 0 || m >= 0x7F800000u ? 0 : 14 - ilogbf(__uint_as_float(m));
-    // 2^sh may leave FP32's range: two factors
-    const int sa = max(-100, min(100, sh));
-    const float fa = pow2(sa), fb = pow2(sh - sa);
-    if (lane == 0) *unshift = ldexpf(1.0f, -sh);
-    constexpr int PC = Geo<FMT>::EL / 8;
-    const int padded = (chunks + PC - 1) / PC * PC;
-    for (int q = lane; q < padded; q += 32) {
-        uint4 o = make_uint4(0, 0, 0, 0);
-        if (q < chunks) {
-            float v[8];
-            load8(row + 8 * q, v);
-            uint32_t h[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 p = __floats2half2_rn(v[2 * i] * fa * fb, v[2 * i + 1] * fa * fb);
-                h[i] = *reinterpret_cast<const uint32_t*>(&p);
-            }
-            o = make_uint4(h[0], h[1], h[2], h[3]);
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = bf16_lo(u[i]);
+            v[2 * i + 1] = bf16_hi(u[i]);
         }
-        *reinterpret_cast<uint4*>(dst + 16 * operand_chunk<FMT>(q)) = o;
+    }
+};
+template <>
+struct Chunk<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float* p) {
+        a = *reinterpret_cast<const float4*>(p);
+        b = *reinterpret_cast<const float4*>(p + 4);
+    }
+    __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+constexpr int STAGE_U = 4;  // chunks of a lane in flight
+
+template <int W>
+__device__ __forceinline__ int warps_per_row(int n) {
+    int wpr = W;
+    while (wpr > 1 && n * wpr > W) wpr >>= 1;
+    return wpr;
+}
+// Whether every lane's chunks fit its registers (one row and one batch each).
+template <int W>
+__device__ __forceinline__ bool staged_from_registers(int n, int K) {
+    const int wpr = warps_per_row<W>(n);
+    return n * wpr <= W && K / 8 <= STAGE_U * 32 * wpr;
+}
+// The loads of a batch: chunks q, q + step, ...
+template <typename In>
+__device__ __forceinline__ void load_chunks(Chunk<In> (&v)[STAGE_U], const In* row, int q, int step, int chunks) {
+#pragma unroll
+    for (int u = 0; u < STAGE_U; ++u) {
+        if (q + u * step < chunks) v[u].load(row + 8 * (q + u * step));
+        else v[u].zero();
     }
 }
+// Ends with the rows visible to all threads. `loaded`: the caller has made
+// the loads (staged_from_registers holds).
+template <int FMT, int W, typename In, typename Src>
+__device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch, float* unshift, uint32_t* amax,
+                                           Chunk<In> (&v)[STAGE_U], bool loaded, Src&& src) {
+    constexpr int PC = Geo<FMT>::EL / 8;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int wpr = warps_per_row<W>(n);
+    const int chunks = K / 8, padded = (chunks + PC - 1) / PC * PC;
+    const int q0 = (warp & (wpr - 1)) * 32 + lane, step = 32 * wpr;
+    const int lw = 31 - __clz(wpr);
+    for (int i = threadIdx.x; i < n; i += 32 * W) amax[i] = 0u;
+    __syncthreads();
+    const bool keep = staged_from_registers<W>(n, K);
+    for (int i = warp >> lw; i < n; i += W >> lw) {
+        const In* row = src(i);
+        uint32_t m = 0;
+        for (int q = q0; q < chunks; q += STAGE_U * step) {
+            if (!loaded) load_chunks(v, row, q, step, chunks);
+#pragma unroll
+            for (int u = 0; u < STAGE_U; ++u) {
+                float f[8];
+                v[u].get(f);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+            }
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
+        if (lane == 0) atomicMax(amax + i, m);
+    }
+    __syncthreads();
+    for (int i = warp >> lw; i < n; i += W >> lw) {
+        const In* row = src(i);
+        const uint32_t m = amax[i];
+        const int sh = m == 0 || m >= 0x7F800000u ? 0 : 14 - ilogbf(__uint_as_float(m));
+        // 2^sh may leave FP32's range: two factors
+        const int sa = max(-100, min(100, sh));
+        const float fa = pow2(sa), fb = pow2(sh - sa);
+        if (q0 == 0) unshift[i] = ldexpf(1.0f, -sh);
+        for (int q = q0; q < padded; q += STAGE_U * step) {
+            if (!keep) load_chunks(v, row, q, step, chunks);
+#pragma unroll
+            for (int u = 0; u < STAGE_U; ++u) {
+                const int c = q + u * step;
+                if (c >= padded) continue;
+                float f[8];
+                v[u].get(f);
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const __half2 p = __floats2half2_rn(f[2 * k] * fa * fb, f[2 * k + 1] * fa * fb);
+                    h[k] = *reinterpret_cast<const uint32_t*>(&p);
+                }
+                // past K: zeros (a second batch there is not what the lane kept)
+                *reinterpret_cast<uint4*>(dst + i * pitch + 16 * operand_chunk<FMT>(c)) =
+                    c < chunks ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(0, 0, 0, 0);
+            }
+        }
+    }
+    __syncthreads();
+}
 
-// The chosen experts in ascending order, and the slots of each.
+// The work on the chosen experts as jobs: an expert with up to `columns` of its
+// slots (the columns of one pass through its weights). An expert with more
+// slots has several jobs, whose weights the L2 cache gives again.
 struct Routing {
-    int* expert;   // [active]
-    int* start;    // [active + 1] first entry of each in slots
-    int* slots;    // [S]
-    int active;
+    int* expert;   // [jobs]
+    int* start;    // [jobs + 1] first entry of each in slots
+    int* slots;    // [S] by expert
+    int* row;      // [S] the slot's operand row: its token (UP) or itself
+    int jobs;
 };
 
-// Built by every CTA from the ids: counts, then a scan over the experts. The
-// order of an expert's slots does not matter (a slot is a column of the MMA).
-__device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem) {
+// Built by every CTA from the ids. Up to 32 slots: one warp, by matching ids;
+// more: counts in shared memory and a scan over the experts. The order of a
+// job's slots does not matter to the results (a slot is a column of the MMA),
+// but which slots make a job has to be the same for all CTAs: where an expert
+// has several jobs, its slots are put in ascending order.
+template <int MODE, int THREADS>
+__device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, int columns) {
     int* count = reinterpret_cast<int*>(mem);                 // [E], then first entries
-    const int most = a.E < a.S ? a.E : a.S;
     Routing r;
     r.expert = count + a.E;
-    r.start = r.expert + most;
-    r.slots = r.start + most + 1;
-    int* active = r.slots + a.S;
+    r.start = r.expert + a.S;
+    r.slots = r.start + a.S + 1;
+    r.row = r.slots + a.S;
+    int* jobs = r.row + a.S;
+    const int lane = threadIdx.x % 32;
+    // `c` slots of expert e, from entry `first` on: lane by lane one more set of jobs
+    auto emit = [&](int e, int c, int first, int at) {
+        for (int k = 0; k < c; k += columns, ++at) {
+            r.expert[at] = e;
+            r.start[at] = first + k;
+        }
+    };
+    auto scan = [&](int v) {
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        return v;
+    };
+    if (a.S <= 32) {
+        if (threadIdx.x < 32) {
+            int e = lane < a.S ? a.ids[lane] : -1;
+            const bool in = e >= 0 && e < a.E;
+            if (lane < a.S && !in && blockIdx.x == 0) atomicOr(a.status, kDevErrBadIndex);
+            if (!in) e = -1;
+            const unsigned same = __match_any_sync(0xffffffffu, e);
+            const int lead = __ffs(same) - 1;
+            const int c = in && lead == lane ? __popc(same) : 0;
+            // slots in the low half, jobs in the high half
+            const int own = c | ((c + columns - 1) / columns) << 16;
+            const int incl = scan(own);
+            emit(e, c, (incl - own) & 0xFFFF, (incl - own) >> 16);
+            const int first = __shfl_sync(0xffffffffu, (incl - own) & 0xFFFF, lead);
+            if (in) {
+                const int at = first + __popc(same & ((1u << lane) - 1u));
+                r.slots[at] = lane;
+                r.row[at] = MODE == UP ? lane / a.topk : lane;
+            }
+            if (lane == 31) {
+                r.start[incl >> 16] = incl & 0xFFFF;
+                *jobs = incl >> 16;
+            }
+        }
+        __syncthreads();
+        r.jobs = *jobs;
+        return r;
+    }
     for (int e = threadIdx.x; e < a.E; e += THREADS) count[e] = 0;
-    __syncthreads();
     int id[MAX_S / THREADS], rank[MAX_S / THREADS];
 #pragma unroll
     for (int i = 0; i < MAX_S / THREADS; ++i) {
         const int s = threadIdx.x + i * THREADS;
-        id[i] = -1;
-        if (s < a.S) {
-            const int e = a.ids[s];
-            if (e >= 0 && e < a.E) {
-                id[i] = e;
-                rank[i] = atomicAdd(&count[e], 1);
-            } else if (blockIdx.x == 0) {
-                atomicOr(a.status, kDevErrBadIndex);
-            }
+        id[i] = s < a.S ? a.ids[s] : -1;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MAX_S / THREADS; ++i) {
+        rank[i] = 0;
+        if (id[i] >= 0 && id[i] < a.E) {
+            rank[i] = atomicAdd(&count[id[i]], 1);
+        } else {
+            if (static_cast<int>(threadIdx.x) + i * THREADS < a.S && blockIdx.x == 0) atomicOr(a.status, kDevErrBadIndex);
+            id[i] = -1;
         }
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int na = 0, tot = 0;
+        int nj = 0, tot = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int c = e0 + lane < a.E ? count[e0 + lane] : 0;
-            const unsigned m = __ballot_sync(0xffffffffu, c > 0);
-            int incl = c;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += v;
-            }
-            if (c > 0) {
-                const int at = na + __popc(m & ((1u << lane) - 1u));
-                r.expert[at] = e0 + lane;
-                r.start[at] = tot + incl - c;
-                count[e0 + lane] = tot + incl - c;
-            }
-            na += __popc(m);
-            tot += __shfl_sync(0xffffffffu, incl, 31);
+            const int own = c | ((c + columns - 1) / columns) << 16;
+            const int incl = scan(own);
+            emit(e0 + lane, c, tot + ((incl - own) & 0xFFFF), nj + ((incl - own) >> 16));
+            if (c > 0) count[e0 + lane] = (tot + ((incl - own) & 0xFFFF)) | c << 16;  // first entry, slots
+            const int all = __shfl_sync(0xffffffffu, incl, 31);
+            nj += all >> 16;
+            tot += all & 0xFFFF;
         }
         if (lane == 0) {
-            r.start[na] = tot;
-            *active = na;
+            r.start[nj] = tot;
+            *jobs = nj;
         }
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < MAX_S / THREADS; ++i)
-        if (id[i] >= 0) r.slots[count[id[i]] + rank[i]] = threadIdx.x + i * THREADS;
-    r.active = *active;
+        if (id[i] >= 0) r.row[(count[id[i]] & 0xFFFF) + rank[i]] = threadIdx.x + i * THREADS;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MAX_S / THREADS; ++i)
+        if (id[i] >= 0) {
+            const int c = count[id[i]] >> 16, s = threadIdx.x + i * THREADS;
+            const int* list = r.row + (count[id[i]] & 0xFFFF);
+            if (c > columns) {
+                int below = 0;
+                for (int k = 0; k < c; ++k) below += list[k] < s;
+                rank[i] = below;
+            }
+        }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < MAX_S / THREADS; ++i)
+        if (id[i] >= 0) {
+            const int s = threadIdx.x + i * THREADS, at = (count[id[i]] & 0xFFFF) + rank[i];
+            r.slots[at] = s;
+            r.row[at] = MODE == UP ? s / a.topk : s;
+        }
+    r.jobs = *jobs;
     __syncthreads();
     return r;
 }
 
-template <int FMT, int MODE, int GMAX>
-__global__ void __launch_bounds__(THREADS, 2) few_kernel(const Args a) {
+template <int FMT, int MODE, int GMAX, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args a) {
     using G = Geo<FMT>;
+    constexpr int THREADS = WARPS * 32, DEPTH = Cta<WARPS>::DEPTH;
+    constexpr int LOG = WARPS == 8 ? 3 : 4;
     using In = typename std::conditional<MODE == UP || MODE == DENSE, __nv_bfloat16, float>::type;
     extern __shared__ __align__(128) uint8_t smem[];
-    const Smem L = smem_layout(G::SLOT, GMAX, a.P, a.pitch, a.E, a.S, MODE != DENSE, MODE == OWN);
+    const Smem L = smem_layout<WARPS>(G::SLOT, GMAX, a.P, a.pitch, a.E, a.S, MODE != DENSE, MODE == OWN);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, t = lane & 3;
     const int N = a.w.N, K = a.w.K;
     const int row_bytes = FMT == FP8 ? K : K / 2;
     const int kp = (row_bytes + 63) / 64;  // pieces per tile of rows
-    float* part = reinterpret_cast<float*>(smem + L.part);
     uint8_t* xs = smem + L.x;
     float* unshift = reinterpret_cast<float*>(smem + L.unshift);
+    uint32_t* amax = reinterpret_cast<uint32_t*>(unshift + a.P);
+    Item* items = reinterpret_cast<Item*>(smem + L.items);
+    const In* in = static_cast<const In*>(a.in);
 
     // UP, DENSE: the ids or the operand may be the previous kernel's output.
     // DOWN, OWN: only the up-projection can still be running (it lets this
@@ -282,250 +465,370 @@ __global__ void __launch_bounds__(THREADS, 2) few_kernel(const Args a) {
         grid_dependency_wait();
         grid_launch_dependents();
     }
-    Routing rt{};
-    if constexpr (MODE == DENSE) rt.active = 1;
-    else rt = build_routing(a, smem + L.route);
-
-    // The rows of this CTA: UP, DOWN, DENSE: an even share of the chosen
-    // experts' rows one after another; OWN: an even share of the output's
-    // rows, for every chosen expert.
-    const int64_t total = MODE == OWN ? N : static_cast<int64_t>(rt.active) * N;
-    const int64_t r0 = total * blockIdx.x / gridDim.x, r1 = total * (blockIdx.x + 1) / gridDim.x;
-    const int first = MODE == OWN ? 0 : static_cast<int>(r0 / N);
-    const int own_tiles = static_cast<int>((r1 - r0 + 15) / 16);
-    const int nseg = r1 <= r0 ? 0 : MODE == OWN ? own_tiles * rt.active : static_cast<int>((r1 - 1) / N) - first + 1;
-    // The warps split K (ks of them share a tile of 16 rows) and, when K is
-    // short and there are tiles enough, the tiles (teams).
-    int ks = WARPS;
-    if (MODE != OWN)
-        while (ks > 1 && kp < 4 * ks && own_tiles >= 8 * WARPS / ks) ks >>= 1;
-    const int teams = WARPS / ks, team = warp / ks, kslice = warp % ks;
-
-    struct Seg { int e, start, n, pb, pe; };
-    auto segment = [&](int s) {
-        Seg sg;
-        int x = 0;
-        if constexpr (MODE == OWN) {
-            x = s % rt.active;
-            sg.pb = static_cast<int>(r0) + 16 * (s / rt.active);
-            sg.pe = min(sg.pb + 16, static_cast<int>(r1));
-        } else {
-            x = first + s;
-            const int64_t b = static_cast<int64_t>(x) * N;
-            sg.pb = static_cast<int>(max(r0 - b, static_cast<int64_t>(0)));
-            sg.pe = static_cast<int>(min(r1 - b, static_cast<int64_t>(N)));
+    // The operand's loads are made early, before the weights fill the memory
+    // system's queues: all tokens (by_token) before the routing, else the first
+    // group's rows after it.
+    Chunk<In> early[STAGE_U];
+    bool loaded = false;
+    auto load_early = [&](int n, auto&& src) {
+        loaded = staged_from_registers<WARPS>(n, K);
+        if (loaded) {
+            const int wpr = warps_per_row<WARPS>(n), i = warp / wpr;
+            if (i < n) load_chunks(early, src(i), (warp % wpr) * 32 + lane, 32 * wpr, K / 8);
         }
-        if constexpr (MODE == DENSE) {
-            sg.e = 0, sg.start = 0, sg.n = a.S;
-        } else {
-            sg.e = rt.expert[x];
-            sg.start = rt.start[x];
-            sg.n = rt.start[x + 1] - sg.start;
-        }
-        return sg;
     };
-    const int pass_rows = min(a.P, 8 * GMAX);
+    const bool by_token = MODE == UP && a.by_token;
+    if (by_token) load_early(a.T, [&](int i) { return in + static_cast<int64_t>(i) * K; });
+
+    const int columns = by_token ? 8 * GMAX : min(a.P, 8 * GMAX);  // of a job
+    Routing rt{};
+    if constexpr (MODE == DENSE) rt.jobs = (a.S + columns - 1) / columns;
+    else rt = build_routing<MODE, THREADS>(a, smem + L.route, columns);
+    auto job_expert = [&](int j) { return MODE == DENSE ? 0 : rt.expert[j]; };
+    auto job_start = [&](int j) { return MODE == DENSE ? min(j * columns, a.S) : rt.start[j]; };
+
+    // The share of this CTA. UP, DOWN, DENSE: tiles of 16 rows, of one job
+    // after another; a segment is a job's part of the share. OWN: rows of the
+    // output, for every job; a segment is up to 16 rows, its tiles the jobs.
+    const int job_tiles = (N + 15) >> 4;
+    int spare, skip = 0, rest;
+    const int each = divide(MODE == OWN ? N : rt.jobs * job_tiles, gridDim.x, a.grid_inv, spare);
+    const int u0 = each * static_cast<int>(blockIdx.x) + min(static_cast<int>(blockIdx.x), spare);
+    const int share = each + (static_cast<int>(blockIdx.x) < spare ? 1 : 0);
+    const int first = MODE == OWN ? 0 : divide(u0, job_tiles, a.tiles_inv, skip);
+    const int nseg = share == 0 || rt.jobs == 0 ? 0
+                     : MODE == OWN              ? (share + 15) >> 4
+                                                : divide(skip + share - 1, job_tiles, a.tiles_inv, rest) + 1;
+    // places [pb, pe) and tiles of a segment
+    auto segment = [&](int s, int& pb, int& pe) {
+        if constexpr (MODE == OWN) {
+            pb = u0 + 16 * s;
+            pe = min(pb + 16, u0 + share);
+            return rt.jobs;
+        } else {
+            const int t0 = s == 0 ? skip : 0;
+            pb = 16 * t0;
+            pe = N;
+            return min(skip + share - s * job_tiles, job_tiles) - t0;
+        }
+    };
+    // Segments are taken in groups whose operand rows are staged together, as
+    // many as fit; the tiles of a group are shared out to the warps without a
+    // barrier. OWN, by_token: all operand rows are staged at the start.
+    auto group_end = [&](int s0) {
+        int s1 = s0 + 1;
+        if (by_token) return nseg;
+        if constexpr (MODE != OWN)
+            while (s1 < nseg && job_start(first + s1 + 1) - job_start(first + s0) <= a.P) ++s1;
+        return s1;
+    };
+
+    // ks warps share a tile's K, so that WARPS / ks teams work on tiles of
+    // their own: the split with the fewest pieces in a row, the joining of a
+    // round's sums counted as one piece (a tile per warp needs none).
+    int ks = 1, lt = LOG;  // teams = 1 << lt
+    {
+        int best = 0x7fffffff, tiles = 0, pb, pe;
+        for (int s = 0; s < nseg && s < 3; ++s) tiles += segment(s, pb, pe);
+        if (MODE == OWN) tiles = rt.jobs;
+#pragma unroll
+        for (int l = 0; l <= LOG; ++l) {
+            const int k = WARPS >> l;
+            const int cost = ((tiles + (1 << l) - 1) >> l) * (((kp + k - 1) >> (LOG - l)) + (k > 1 ? 1 : 0));
+            if (cost < best) best = cost, ks = k, lt = l;
+        }
+    }
+    const int teams = 1 << lt, team = warp >> (LOG - lt), kslice = warp & (ks - 1);
 
     // ---- weight stream: this warp's pieces in order, DEPTH of them in flight
-    // in lane-private places of the ring (a lane reads back what it copied)
+    // in lane-private places of the ring (a lane reads back what it copied).
+    // Rows past the segment repeat its first row (their sums are not stored);
+    // bytes past the end of a row are zeros.
+    const int pieces = kslice < kp ? (kp - kslice + ks - 1) >> (LOG - lt) : 0;  // of a tile, for this warp
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * DEPTH * G::SLOT);
-    int is = -1, ipass = 0, inpass = 0, itile = 0, intiles = 0, ik = kp;  // the next piece to request
-    Seg iseg{};
-    const uint8_t* wp[2];
-    const uint8_t* sp[2];
-    bool wv[2] = {false, false};
-    auto request = [&](int slot) {
-        if (ik >= kp) {  // next tile of this team
-            itile += teams;
-            while (itile >= intiles) {
-                if (++ipass >= inpass) {
-                    if (++is >= nseg) break;
-                    iseg = segment(is);
-                    ipass = 0;
-                    inpass = (iseg.n + pass_rows - 1) / pass_rows;
-                    intiles = (iseg.pe - iseg.pb + 15) / 16;
-                }
-                itile = team;
+    int rseg = -1, rgroup = 0, rtile = team - teams, rtiles = 0, rpb = 0, rpe = 0, rleft = 0, rrem = 0;
+    const uint8_t *wp0 = nullptr, *wp1 = nullptr, *sp0 = nullptr, *sp1 = nullptr;
+    auto next_tile = [&](uint32_t place) {
+        rtile += teams;
+        while (rtile >= rtiles) {
+            rtile -= rtiles;
+            if (++rseg >= nseg) {
+                rseg = nseg, rtiles = 0x7fffffff;
+                return;
             }
-            ik = kslice;
-            if (is < nseg) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int p = iseg.pb + 16 * itile + 8 * h + g;
-                    wv[h] = p < iseg.pe;
-                    const int64_t row = static_cast<int64_t>(iseg.e) * N + place_to_row<FMT>(wv[h] ? p : iseg.pb);
-                    wp[h] = a.w.q + row * row_bytes + 16 * t;
-                    if constexpr (FMT == NVFP4)
-                        sp[h] = a.w.sf + ((row >> 7) * (K / 64) + (t >> 1)) * 512 + 16 * (row & 31) + 4 * ((row & 127) >> 5);
-                }
-            } else {
-                ik = kp;
-                itile = 0, intiles = 0, ipass = 0, inpass = 0;  // nothing left: stay here
-                is = nseg;
+            if (rseg == rgroup) {
+                rgroup = group_end(rseg);
+                rtile = team;
             }
+            rtiles = segment(rseg, rpb, rpe);
         }
-        if (is < nseg && ik < kp) {
-            const uint32_t dst = ring + slot * G::SLOT + 16 * lane;
-            const bool in = 64 * ik + 16 * t < row_bytes;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const bool v = wv[h] && in;
-                cp_async16(dst + 512 * h, v ? wp[h] + 64 * ik : a.w.q, v);
-                if constexpr (FMT == NVFP4)
-                    cp_async4(ring + slot * G::SLOT + 1024 + 128 * h + 4 * lane, v ? sp[h] + 1024 * static_cast<int64_t>(ik) : a.w.sf, v);
+        const int e = job_expert(MODE == OWN ? rtile : first + rseg);
+        const int p = rpb + (MODE == OWN ? 0 : 16 * rtile) + g;
+        const uint32_t row0 = static_cast<uint32_t>(e * N + place_to_row<FMT>(p < rpe ? p : rpb));
+        const uint32_t row1 = static_cast<uint32_t>(e * N + place_to_row<FMT>(p + 8 < rpe ? p + 8 : rpb));
+        const int at = 64 * kslice + 16 * t;
+        wp0 = a.w.q + static_cast<uint64_t>(row0) * static_cast<uint32_t>(row_bytes) + at;
+        wp1 = a.w.q + static_cast<uint64_t>(row1) * static_cast<uint32_t>(row_bytes) + at;
+        rrem = row_bytes - at;
+        rleft = pieces;
+        if constexpr (FMT == FP8) {
+            cp_async4(place + 1024 + 4 * lane, a.w.s + row0, false);
+            cp_async4(place + 1152 + 4 * lane, a.w.s + row1, false);
+        } else {
+            auto scales = [&](uint32_t row) {
+                return a.w.sf + static_cast<uint64_t>((row >> 7) * (K / 64) + 2 * kslice + (t >> 1)) * 512 + 16 * (row & 31) +
+                       4 * ((row & 127) >> 5);
+            };
+            sp0 = scales(row0);
+            sp1 = scales(row1);
+            cp_async4(place + 1280 + 4 * lane, a.w.s + e, false);
+        }
+    };
+    auto request = [&](uint32_t place) {
+        if (rleft == 0 && rseg < nseg) next_tile(place);
+        if (rleft > 0) {
+            const bool past = rrem <= 0;
+            cp_async16(place + 16 * lane, wp0, past);
+            cp_async16(place + 512 + 16 * lane, wp1, past);
+            wp0 += 64 * ks;
+            wp1 += 64 * ks;
+            if constexpr (FMT == NVFP4) {
+                cp_async4(place + 1024 + 4 * lane, sp0, past);
+                cp_async4(place + 1152 + 4 * lane, sp1, past);
+                sp0 += 1024 * ks;
+                sp1 += 1024 * ks;
             }
-            ik += ks;
+            rrem -= 64 * ks;
+            --rleft;
         }
         cp_async_commit();
     };
-    for (int d = 0; d < DEPTH; ++d) request(d);
-    int slot = 0;
+    if (pieces == 0) rseg = nseg;
+    if constexpr (MODE == UP || MODE == DENSE) {
+        if (!by_token && nseg > 0) {
+            const int base = job_start(first);
+            load_early(job_start(first + group_end(0)) - base,
+                       [&](int i) { return in + static_cast<int64_t>(MODE == DENSE ? base + i : rt.row[base + i]) * K; });
+        }
+    }
+    // fill the ring: the first tile's pieces side by side, then the next tiles'
+    if (rseg < nseg) next_tile(ring);
+    const int ahead = min(rleft, DEPTH);
+#pragma unroll
+    for (int d = 0; d < DEPTH; ++d) {
+        if (d < ahead) {
+            const uint32_t to = ring + d * G::SLOT;
+            const int off = 64 * ks * d;
+            const bool past = rrem <= off;
+            cp_async16(to + 16 * lane, wp0 + off, past);
+            cp_async16(to + 512 + 16 * lane, wp1 + off, past);
+            if constexpr (FMT == NVFP4) {
+                cp_async4(to + 1024 + 4 * lane, sp0 + 16 * off, past);
+                cp_async4(to + 1152 + 4 * lane, sp1 + 16 * off, past);
+            }
+            cp_async_commit();
+        }
+    }
+    wp0 += 64 * ks * ahead;
+    wp1 += 64 * ks * ahead;
+    if constexpr (FMT == NVFP4) {
+        sp0 += 1024 * ks * ahead;
+        sp1 += 1024 * ks * ahead;
+    }
+    rrem -= 64 * ks * ahead;
+    rleft -= ahead;
+#pragma unroll 1
+    for (int d = ahead; d < DEPTH; ++d) request(ring + d * G::SLOT);
+    uint32_t place = ring;  // of the oldest piece
 
     if constexpr (MODE == DOWN || MODE == OWN) {
         grid_dependency_wait();
         grid_launch_dependents();
     }
-    // ---- operand rows
-    auto stage = [&](int start, int n) {
-        for (int i = warp; i < n; i += WARPS) {
-            const int s = MODE == DENSE ? start + i : rt.slots[start + i];
-            const int64_t r = MODE == UP ? s / a.topk : s;
-            stage_row<FMT>(static_cast<const In*>(a.in) + r * K, K, xs + i * a.pitch, unshift + i, lane);
-        }
-    };
-    if constexpr (MODE == OWN) {
-        stage(0, rt.active ? rt.start[rt.active] : 0);
-        __syncthreads();
-    }
-
     int buf = 0;
-    for (int s = 0; s < nseg; ++s) {
-        const Seg sg = segment(s);
-        const int ntiles = (sg.pe - sg.pb + 15) / 16;
-        for (int p0 = 0; p0 < sg.n; p0 += pass_rows) {
-            const int n = min(pass_rows, sg.n - p0);
-            const int ng = (n + 7) / 8;
-            const int xrow0 = MODE == OWN ? sg.start + p0 : 0;
-            if constexpr (MODE != OWN) {
-                __syncthreads();
-                stage(sg.start + p0, n);
-                __syncthreads();
-            }
-            for (int tile0 = 0; tile0 < ntiles; tile0 += teams) {
-                float acc[GMAX][4];
+    for (int s0 = 0; s0 < nseg;) {
+        const int s1 = group_end(s0);
+        // ---- operand rows, in the order of the slot list (OWN: those of slots
+        // without an expert are not in it), or the tokens
+        const int base = MODE == OWN ? 0 : job_start(first + s0);
+        if (!(MODE == OWN || by_token) || s0 == 0) {
+            if (s0 > 0) __syncthreads();
+            const int n = by_token ? a.T : job_start(MODE == OWN ? rt.jobs : first + s1) - base;
+            stage_rows<FMT, WARPS, In>(n, K, xs, a.pitch, unshift, amax, early, loaded, [&](int i) {
+                return in + static_cast<int64_t>(by_token ? i : MODE == DENSE ? base + i : rt.row[base + i]) * K;
+            });
+            loaded = false;
+        }
+        int tiles = 0, pb = 0, pe = 0;
+        for (int s = s0; s < s1; ++s) tiles += segment(s, pb, pe);
+        int cs = s0, ct = team, ctiles = segment(s0, pb, pe);  // this team's tile
+        for (int tile0 = 0; tile0 < tiles; tile0 += teams, ct += teams) {
+            const bool mine = tile0 + team < tiles;
+            // one group of columns: two chains of MMAs, added at the end
+            constexpr int CHAINS = GMAX == 1 ? 2 : 1;
+            float acc[GMAX * CHAINS][4];
 #pragma unroll
-                for (int q = 0; q < GMAX; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
-                if (tile0 + team < ntiles) {
-                    for (int k = kslice; k < kp; k += ks) {
-                        cp_async_wait_oldest();
-                        const uint8_t* src = smem + warp * DEPTH * G::SLOT + slot * G::SLOT;
-                        const uint4 wa = *reinterpret_cast<const uint4*>(src + 16 * lane);
-                        const uint4 wb = *reinterpret_cast<const uint4*>(src + 512 + 16 * lane);
-                        uint32_t sa = 0, sb = 0;
-                        if constexpr (FMT == NVFP4) {
-                            sa = *reinterpret_cast<const uint32_t*>(src + 1024 + 4 * lane) >> (16 * (t & 1));
-                            sb = *reinterpret_cast<const uint32_t*>(src + 1152 + 4 * lane) >> (16 * (t & 1));
-                        }
-                        // the piece's weights as the MMAs' A operand: rows g, g + 8; four K elements a step
-                        constexpr int STEPS = G::EL / 16;
-                        uint32_t A[STEPS][4];
-                        if constexpr (FMT == FP8) {
-                            const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                e4m3x4_to_f16(va[i], A[i][0], A[i][2]);
-                                e4m3x4_to_f16(vb[i], A[i][1], A[i][3]);
-                            }
-                        } else {
-                            const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
-                            uint32_t fa[2], fb[2];
-                            scale_pairs(sa, fa[0], fa[1]);
-                            scale_pairs(sb, fb[0], fb[1]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                uint32_t ha[4], hb[4];
-                                e2m1x8_to_f16(va[i], ha);
-                                e2m1x8_to_f16(vb[i], hb);
-#pragma unroll
-                                for (int j = 0; j < 2; ++j) {
-                                    A[2 * i + j][0] = mul_f16x2(ha[2 * j], fa[i / 2]);
-                                    A[2 * i + j][2] = mul_f16x2(ha[2 * j + 1], fa[i / 2]);
-                                    A[2 * i + j][1] = mul_f16x2(hb[2 * j], fb[i / 2]);
-                                    A[2 * i + j][3] = mul_f16x2(hb[2 * j + 1], fb[i / 2]);
-                                }
-                            }
-                        }
-                        request(slot);
-                        slot = slot + 1 == DEPTH ? 0 : slot + 1;
-#pragma unroll
-                        for (int q = 0; q < GMAX; ++q) {
-                            if (q >= ng) break;
-                            const bool have = 8 * q + g < n;
-                            const uint8_t* xr = xs + (xrow0 + 8 * q + g) * a.pitch + k * (2 * G::EL) + 16 * t;
-#pragma unroll
-                            for (int i = 0; i < G::CH; ++i) {
-                                uint4 xv = make_uint4(0, 0, 0, 0);
-                                if (have) xv = *reinterpret_cast<const uint4*>(xr + 64 * i);
-                                mma_16816(acc[q], A[2 * i][0], A[2 * i][1], A[2 * i][2], A[2 * i][3], xv.x, xv.y);
-                                mma_16816(acc[q], A[2 * i + 1][0], A[2 * i + 1][1], A[2 * i + 1][2], A[2 * i + 1][3], xv.z, xv.w);
-                            }
-                        }
-                    }
+            for (int q = 0; q < GMAX * CHAINS; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
+            int start = 0, n = 0;
+            if (mine) {
+                while (ct >= ctiles) {
+                    ct -= ctiles;
+                    ctiles = segment(++cs, pb, pe);
                 }
-                // ---- the warps' sums meet in shared memory, added in a fixed order
-                float* pb = part + buf * (WARPS * 128 * GMAX);
+                const int j = MODE == OWN ? ct : first + cs;
+                start = job_start(j);
+                n = job_start(j + 1) - start;
+                // columns past n repeat the first one: their sums are not stored
+                auto column = [&](int c) {
+                    const int at = start + (c < n ? c : 0);
+                    return by_token ? rt.row[at] : at - base;
+                };
+                uint32_t xp[GMAX];
 #pragma unroll
                 for (int q = 0; q < GMAX; ++q)
-                    if (q < ng)
-                        *reinterpret_cast<float4*>(pb + (warp * GMAX + q) * 128 + 4 * lane) =
-                            make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
-                __syncthreads();
-                for (int o = threadIdx.x; o < teams * ng * 128; o += THREADS) {
-                    const int tm = o / (ng * 128), q = (o >> 7) % ng, at = o & 127;
-                    const int ln = at >> 2, comp = at & 3;
-                    const int col = 8 * q + 2 * (ln & 3) + (comp & 1);
-                    const int p = sg.pb + 16 * (tile0 + tm) + (ln >> 2) + 8 * (comp >> 1);
-                    if (col >= n || p >= sg.pe) continue;
-                    float sum = 0.0f;
-                    for (int w = 0; w < ks; ++w) sum += pb[((tm * ks + w) * GMAX + q) * 128 + at];
-                    const int row = place_to_row<FMT>(p);
-                    const float sc = FMT == FP8 ? a.w.s[static_cast<int64_t>(sg.e) * N + row] : a.w.s[sg.e];
-                    const float v = sum * unshift[xrow0 + col] * sc;
-                    if constexpr (MODE == DENSE) {
-                        static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(p0 + col) * N + row] = __float2bfloat16_rn(v);
-                    } else {
-                        const int sl = rt.slots[sg.start + p0 + col];
-                        if constexpr (MODE == OWN) reinterpret_cast<float*>(smem + L.own)[sl * 16 + (p - sg.pb)] = v;
-                        else static_cast<float*>(a.out)[static_cast<int64_t>(sl) * N + row] = v;
-                    }
+                    xp[q] = smem_u32(xs) + column(8 * q + g) * a.pitch + kslice * (2 * G::EL) + 16 * t;
+                float sr[2] = {0.0f, 0.0f};
+                if (pieces > 0) {
+                    cp_async_wait_oldest<DEPTH>();
+                    sr[0] = __uint_as_float(ld_shared4(place + (FMT == FP8 ? 1024 : 1280) + 4 * lane));
+                    sr[1] = FMT == FP8 ? __uint_as_float(ld_shared4(place + 1152 + 4 * lane)) : sr[0];
                 }
-                buf ^= 1;
+                auto run = [&](auto groups) {
+                    constexpr int NG = decltype(groups)::value;
+#pragma unroll 1
+                    for (int i = 0; i < pieces; ++i) {
+                        cp_async_wait_oldest<DEPTH>();
+                        const uint4 wa = ld_shared16(place + 16 * lane), wb = ld_shared16(place + 512 + 16 * lane);
+                        uint32_t fa[2] = {0, 0}, fb[2] = {0, 0};
+                        if constexpr (FMT == NVFP4) {
+                            scale_pairs(ld_shared4(place + 1024 + 4 * lane) >> (16 * (t & 1)), fa[0], fa[1]);
+                            scale_pairs(ld_shared4(place + 1152 + 4 * lane) >> (16 * (t & 1)), fb[0], fb[1]);
+                        }
+                        const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
+                        // a chunk of 8 elements of K per lane at a time: rows g and g + 8 as the A
+                        // operand of two MMAs (4 elements of K each), every group of 8 columns
+#pragma unroll
+                        for (int c = 0; c < G::CH; ++c) {
+                            uint32_t A[2][4];
+                            if constexpr (FMT == FP8) {
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    e4m3x4_to_f16(va[2 * c + j], A[j][0], A[j][2]);
+                                    e4m3x4_to_f16(vb[2 * c + j], A[j][1], A[j][3]);
+                                }
+                            } else {
+                                uint32_t ha[4], hb[4];
+                                e2m1x8_to_f16(va[c], ha);
+                                e2m1x8_to_f16(vb[c], hb);
+#pragma unroll
+                                for (int j = 0; j < 2; ++j) {
+                                    A[j][0] = mul_f16x2(ha[2 * j], fa[c / 2]);
+                                    A[j][2] = mul_f16x2(ha[2 * j + 1], fa[c / 2]);
+                                    A[j][1] = mul_f16x2(hb[2 * j], fb[c / 2]);
+                                    A[j][3] = mul_f16x2(hb[2 * j + 1], fb[c / 2]);
+                                }
+                            }
+#pragma unroll
+                            for (int q = 0; q < NG; ++q) {
+                                const uint4 xv = ld_shared16(xp[q] + 64 * c);
+                                mma_16816(acc[q], A[0][0], A[0][1], A[0][2], A[0][3], xv.x, xv.y);
+                                mma_16816(acc[GMAX * (CHAINS - 1) + q], A[1][0], A[1][1], A[1][2], A[1][3], xv.z, xv.w);
+                            }
+                        }
+#pragma unroll
+                        for (int q = 0; q < NG; ++q) xp[q] += ks * (2 * G::EL);
+                        request(place);
+                        place = place == ring + (DEPTH - 1) * G::SLOT ? ring : place + G::SLOT;
+                    }
+                };
+                if (GMAX == 1 || n <= 8) run(std::integral_constant<int, 1>());
+                else if (GMAX == 2 || n <= 16) run(std::integral_constant<int, GMAX < 2 ? GMAX : 2>());
+                else run(std::integral_constant<int, GMAX>());
+                if constexpr (CHAINS == 2) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) acc[0][j] += acc[1][j];
+                }
+                // scales: of the rows, and of the columns' operand rows
+#pragma unroll
+                for (int q = 0; q < GMAX; ++q)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float u = unshift[column(8 * q + 2 * t + j)];
+                        acc[q][j] = acc[q][j] * u * sr[0];
+                        acc[q][2 + j] = acc[q][2 + j] * u * sr[1];
+                    }
+            }
+            // value v of column c of the job whose slots start at `at`, at place p
+            auto put = [&](int at, int c, int p, float v) {
+                const int row = place_to_row<FMT>(p);
+                if constexpr (MODE == DENSE) {
+                    static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(at + c) * N + row] = __float2bfloat16_rn(v);
+                } else {
+                    const int sl = rt.slots[at + c];
+                    if constexpr (MODE == OWN) reinterpret_cast<float*>(smem + L.own)[sl * 16 + (p - u0 - 16 * s0)] = v;
+                    else static_cast<float*>(a.out)[static_cast<int64_t>(sl) * N + row] = v;
+                }
+            };
+            const int p0 = pb + (MODE == OWN ? 0 : 16 * ct);
+            if (ks == 1) {
+                if (mine) {
+#pragma unroll
+                    for (int q = 0; q < GMAX; ++q)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int c = 8 * q + 2 * t + (j & 1), p = p0 + g + 8 * (j >> 1);
+                            if (c < n && p < pe) put(start, c, p, acc[q][j]);
+                        }
+                }
+            } else {
+                // ---- the warps' sums meet in shared memory, added in a fixed order
+                float* part = reinterpret_cast<float*>(smem + L.part) + buf * (WARPS * 128 * GMAX);
+                if (mine) {
+#pragma unroll
+                    for (int q = 0; q < GMAX; ++q)
+                        if (8 * q < n)
+                            *reinterpret_cast<float4*>(part + (warp * GMAX + q) * 128 + 4 * lane) =
+                                make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
+                }
+                if (kslice == 0 && lane == 0) items[buf * WARPS + team] = Item{start, mine ? n : 0, p0, pe};
+                __syncthreads();
+                for (int o = threadIdx.x; o < teams * GMAX * 128; o += THREADS) {
+                    const int tm = o / (GMAX * 128), q = (o >> 7) % GMAX, at = o & 127;
+                    const Item it = items[buf * WARPS + tm];
+                    const int c = 8 * q + 2 * ((at >> 2) & 3) + (at & 1), p = it.p + (at >> 4) + 8 * ((at >> 1) & 1);
+                    if (c >= it.n || p >= it.pe) continue;
+                    float sum = 0.0f;
+                    for (int w = 0; w < ks; ++w) sum += part[((tm * ks + w) * GMAX + q) * 128 + at];
+                    put(it.slot0, c, p, sum);
+                }
+                if constexpr (GMAX == 1) buf ^= 1;
+                else __syncthreads();  // one buffer
             }
         }
         if constexpr (MODE == OWN) {
-            if (s % rt.active == rt.active - 1) {
-                // every chosen expert has given its part of these rows
-                __syncthreads();
-                const float* ov = reinterpret_cast<const float*>(smem + L.own);
-                for (int i = threadIdx.x; i < a.T * 16; i += THREADS) {
-                    const int tk = i >> 4, p = sg.pb + (i & 15);
-                    if (p >= sg.pe) continue;
-                    float y = 0.0f;
-                    for (int j = 0; j < a.topk; ++j) {
-                        const int sl = tk * a.topk + j;
-                        const int e = a.ids[sl];
-                        if (e >= 0 && e < a.E) y = fmaf(a.tw[sl], ov[sl * 16 + (i & 15)], y);
-                    }
-                    static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(tk) * N + place_to_row<FMT>(p)] = __float2bfloat16_rn(y);
+            // every job has given its part of these 16 rows
+            __syncthreads();
+            const float* ov = reinterpret_cast<const float*>(smem + L.own);
+            segment(s0, pb, pe);
+            for (int i = threadIdx.x; i < a.T * 16; i += THREADS) {
+                const int tk = i >> 4, p = pb + (i & 15);
+                if (p >= pe) continue;
+                float y = 0.0f;
+                for (int j = 0; j < a.topk; ++j) {
+                    const int sl = tk * a.topk + j;
+                    const int id = a.ids[sl];
+                    if (id >= 0 && id < a.E) y = fmaf(a.tw[sl], ov[sl * 16 + (i & 15)], y);
                 }
-                __syncthreads();
+                static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(tk) * N + place_to_row<FMT>(p)] = __float2bfloat16_rn(y);
             }
+            __syncthreads();
         }
+        s0 = s1;
     }
     if constexpr (MODE == OWN) {
-        if (rt.active == 0) {  // no token has an expert
-            for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < static_cast<int64_t>(a.T) * N;
-                 i += static_cast<int64_t>(gridDim.x) * THREADS)
+        if (rt.jobs == 0) {  // no token has an expert
+            for (int i = static_cast<int>(blockIdx.x) * THREADS + threadIdx.x; i < a.T * N;
+                 i += static_cast<int>(gridDim.x) * THREADS)
                 static_cast<__nv_bfloat16*>(a.out)[i] = __float2bfloat16_rn(0.0f);
         }
     }
@@ -567,39 +870,55 @@ int check_moe(const char* name, int act, int64_t T, int64_t topk, int64_t E, int
     return METIS_OK;
 }
 
-// Launches few_kernel with as much of the operand staged as fits: two CTAs per
-// SM when at least `want` rows (or 8) fit beside the ring, else one.
-template <int FMT, int MODE, int GMAX>
-int launch_few(const DeviceInfo& di, Args a, int want, cudaStream_t st) {
+// Launches few_kernel with as many staged operand rows as are of use (OWN: all
+// slots; else the columns of two jobs) and fit. CTAs of 8 warps go two per SM
+// (for `latency` one, which leaves the other place to the next kernel).
+template <int FMT, int MODE, int GMAX, int W>
+int launch_few(const DeviceInfo& di, Args a, bool latency, cudaStream_t st) {
     using G = Geo<FMT>;
     static std::atomic<uint64_t> done[64];
     int rc = once_per_context(done, di.device, [&] {
-        return cuda_check(cudaFuncSetAttribute(few_kernel<FMT, MODE, GMAX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cuda_check(cudaFuncSetAttribute(few_kernel<FMT, MODE, GMAX, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                di.max_smem_optin),
                           "cudaFuncSetAttribute(few tokens)");
     });
     if (rc) return rc;
-    a.pitch = (a.w.K + G::EL - 1) / G::EL * G::EL * 2 + 64;
+    a.pitch = operand_pitch<FMT>(a.w.K);
     constexpr int HALF = 112 * 1024;  // two CTAs per SM
-    auto bytes = [&](int P) { return smem_layout(G::SLOT, GMAX, P, a.pitch, a.E, a.S, MODE != DENSE, MODE == OWN).total; };
-    const int base = bytes(0) + 16;
-    int P = (HALF - base) / (a.pitch + 4), per_sm = 2;
-    if (P < want && P < 8) {
-        P = (di.max_smem_optin - base) / (a.pitch + 4);
-        per_sm = 1;
+    auto bytes = [&](int P) { return smem_layout<W>(G::SLOT, GMAX, P, a.pitch, a.E, a.S, MODE != DENSE, MODE == OWN).total; };
+    const int base = bytes(0) + 32;  // rounding
+    const int half = (HALF - base) / (a.pitch + 8), full = (di.max_smem_optin - base) / (a.pitch + 8);
+    const int per_job = a.T < 8 * GMAX ? a.T : 8 * GMAX;
+    const int want = MODE == OWN || a.S < 2 * per_job ? a.S : 2 * per_job;
+    int per_sm = 1;
+    a.P = want < full ? want : full;
+    if (W == 8) {
+        const int least = MODE == OWN || want < 8 ? want : 8;
+        if (half >= least) {
+            per_sm = latency ? 1 : 2;
+            a.P = want < half ? want : half;
+        }
     }
-    if (P < 1 || (MODE == OWN && P < want)) return fail(METIS_ERR_UNSUPPORTED, "few-token kernel: K=%d too long", a.w.K);
-    a.P = P < want ? P : want;
-    return cuda_check(launch_pdl(few_kernel<FMT, MODE, GMAX>, dim3(di.num_sms * per_sm), dim3(THREADS), bytes(a.P), st, 1, a),
+    if (a.P < 1 || (MODE == OWN && a.P < want))
+        return fail(METIS_ERR_UNSUPPORTED, "few-token kernel: K=%d is too long", a.w.K);
+    // a few tokens that all threads read with one round trip
+    a.by_token = MODE == UP && a.T <= a.P && a.T <= W && static_cast<int64_t>(a.T) * a.w.K <= 8 * STAGE_U * 32 * W;
+    a.grid_inv = 0xFFFFFFFFu / static_cast<uint32_t>(di.num_sms * per_sm);
+    a.tiles_inv = 0xFFFFFFFFu / static_cast<uint32_t>((a.w.N + 15) / 16);
+    return cuda_check(launch_pdl(few_kernel<FMT, MODE, GMAX, W>, dim3(di.num_sms * per_sm), dim3(W * 32), bytes(a.P), st, 1, a),
                       "few-token kernel launch");
 }
 
-// By the tokens that one pass multiplies (8, 16 or 32).
+// By the columns that one pass multiplies (8, 16 or 32), the weight bytes that
+// an SM reads, and what fits beside long rows.
 template <int FMT, int MODE>
-int launch_few_by_rows(const DeviceInfo& di, const Args& a, int rows, int want, cudaStream_t st) {
-    if (rows <= 8) return launch_few<FMT, MODE, 1>(di, a, want, st);
-    if (rows <= 16) return launch_few<FMT, MODE, 2>(di, a, want, st);
-    return launch_few<FMT, MODE, 4>(di, a, want, st);
+int launch_few_by_size(const DeviceInfo& di, const Args& a, int columns, int64_t weight_bytes, cudaStream_t st) {
+    const bool small = weight_bytes < di.num_sms * 160ll * 1024;
+    const bool long_rows = operand_pitch<FMT>(a.w.K) * 8 > 112 * 1024;
+    if ((columns <= 8 && small) || long_rows) return launch_few<FMT, MODE, 1, 8>(di, a, true, st);
+    if (columns <= 8) return launch_few<FMT, MODE, 1, 16>(di, a, false, st);
+    if (columns <= 16) return launch_few<FMT, MODE, 2, 16>(di, a, false, st);
+    return launch_few<FMT, MODE, 4, 16>(di, a, false, st);
 }
 
 template <int FMT>
@@ -620,19 +939,20 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
     a.T = T;
     a.topk = topk;
     a.out = h;
-    const int rows = S < T ? S : T;  // of one expert, unless a token names it twice
-    const int most = rows <= 8 ? 8 : rows <= 16 ? 16 : 32;
-    if ((rc = launch_few_by_rows<FMT, UP>(di, a, rows, S < most ? S : most, st))) return rc;
+    // columns of an expert: about twice the mean number of its slots, at most the tokens
+    const int likely = 2 * S / E + 4;
+    const int columns = likely < T ? likely : T;
+    const int64_t weight_bytes = static_cast<int64_t>(S < E ? S : E) * up.N * up.K / (FMT == FP8 ? 1 : 2);
+    if ((rc = launch_few_by_size<FMT, UP>(di, a, columns, weight_bytes, st))) return rc;
     a.in = h;
     a.w = down;
     // few slots: every CTA stages all of h and owns rows of the output
-    const int pitch = (down.K + Geo<FMT>::EL - 1) / Geo<FMT>::EL * Geo<FMT>::EL * 2 + 64;
-    if (S <= 64 && S * pitch <= 40 * 1024) {
+    if (S <= 64 && S * operand_pitch<FMT>(down.K) <= 40 * 1024) {
         a.out = y;
-        return launch_few<FMT, OWN, 1>(di, a, S, st);
+        return launch_few<FMT, OWN, 1, 8>(di, a, true, st);
     }
     a.out = o;
-    if ((rc = launch_few_by_rows<FMT, DOWN>(di, a, rows, S < most ? S : most, st))) return rc;
+    if ((rc = launch_few_by_size<FMT, DOWN>(di, a, columns, weight_bytes, st))) return rc;
     return cuda_check(launch_pdl(combine_kernel, dim3((down.N + 255) / 256, T), dim3(256), 0, st, 1,
                                  static_cast<const float*>(o), ids, tw, topk, E, down.N, y),
                       "few-token combine launch");
@@ -731,6 +1051,5 @@ extern "C" int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, con
     a.S = a.T = static_cast<int>(M);
     a.topk = 1;
     a.out = y_bf16;
-    const int rows = static_cast<int>(M < 32 ? M : 32);
-    return few::launch_few_by_rows<few::NVFP4, few::DENSE>(di, a, rows, rows, static_cast<cudaStream_t>(stream));
+    return few::launch_few_by_size<few::NVFP4, few::DENSE>(di, a, a.S, N * K / 2, static_cast<cudaStream_t>(stream));
 }
