@@ -106,6 +106,11 @@ int launch_nvfp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* ga, in
                       __nv_bfloat16* y, const int32_t* offsets, const int32_t* counts, int E, int M,
                       int N, int K, cudaStream_t st);
 
+// MXFP4 block-scaled GEMM (nvfp4.cu): codes and tiled E8M0 scales, a_rows and
+// b_rows multiples of 128.
+int launch_mxfp4_gemm(const uint8_t* qa, const uint8_t* sfa, int64_t a_rows, const uint8_t* qb, const uint8_t* sfb,
+                      int64_t b_rows, __nv_bfloat16* y, int M, int N, int K, cudaStream_t st);
+
 // BF16 GEMM y = bf16(a b^T) (gemm_fp8.cu); s_b non-null scales column n:
 // y = bf16(fl32((a b^T)[., n] * s_b[n])).
 int launch_bf16_gemm(const __nv_bfloat16* a, const __nv_bfloat16* b, __nv_bfloat16* y, int M, int N,

@@ -1,6 +1,7 @@
 // MXFP4 (OCP Microscaling specification 1.0) on sm_100a: E2M1 codes with one
-// power-of-two scale (E8M0) per 32 elements. Quantization, reading back, and
-// the product of two MXFP4 matrices.
+// power-of-two scale (E8M0) per 32 elements. Quantization and reading back
+// here; the product of two MXFP4 matrices is the block-scaled GEMM of
+// nvfp4.cu with kind::mxf4.
 #include "common.cuh"
 #include "../../include/metis_mxfp4.h"
 
@@ -10,21 +11,6 @@ namespace mxfp4 {
 // Byte offset of the scale of row r, block b in the tiled layout (kc = K / 128 atoms per 128 rows).
 __host__ __device__ __forceinline__ int64_t tiled_offset(int64_t r, int64_t b, int64_t kc) {
     return ((r >> 7) * kc + (b >> 2)) * 512 + 16 * (r & 31) + 4 * ((r & 127) >> 5) + (b & 3);
-}
-
-__device__ __forceinline__ float load_value(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ float load_value(const float* p) { return *p; }
-
-__device__ __forceinline__ uint32_t e2m1_pair(float lo, float hi) {
-    uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tmov.b32 %0, {b, b, b, b};\n\t}"
-        : "=r"(r) : "f"(lo), "f"(hi));
-    return r & 0xFFu;
-}
-
-__device__ __forceinline__ float e2m1_value(uint32_t n) {
-    const float mag = (n & 6u) == 0 ? 0.5f * (n & 1u) : (1.0f + 0.5f * (n & 1u)) * static_cast<float>(1u << ((n >> 1 & 3u) - 1u));
-    return n & 8u ? -mag : mag;
 }
 
 __device__ __forceinline__ float e8m0_value(uint32_t c) {
@@ -39,66 +25,180 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t amax_bits) {
     return e < 0 ? 0u : static_cast<uint32_t>(e);
 }
 
-// One thread per block of 32 elements.
+// Half a block, 16 consecutive elements: a lane's share. Two lanes make a
+// block, eight a group of four blocks (128 elements, whose scales are one
+// 32-bit word in both layouts).
 template <typename T>
-__global__ void __launch_bounds__(256) quant_kernel(const T* x, int64_t R, int64_t K, int64_t ldx, uint8_t* q,
-                                                    uint8_t* sf, int tiled, int64_t rows) {
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int64_t nb = K / 32;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= rows * nb) return;
-    const int64_t r = i / nb, b = i - r * nb;
-    const int64_t at = tiled ? tiled_offset(r, b, K / 128) : i;
-    if (r >= R) {
-        sf[at] = 0;
-        return;
+struct Half;
+template <>
+struct Half<__nv_bfloat16> {
+    uint4 w[2];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+        w[0] = __ldg(reinterpret_cast<const uint4*>(p));
+        w[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
     }
-    const T* p = x + r * ldx + 32 * b;
-    uint32_t m = 0;
-    for (int k = 0; k < 32; ++k) m = max(m, __float_as_uint(load_value(p + k)) & 0x7FFFFFFFu);
-    const uint32_t c = scale_code(m);
-    const float inv = c == 255u ? 0.0f : __uint_as_float((254u - c) << 23);
-    for (int k = 0; k < 32; k += 2) {
-        const float v0 = __fmul_rn(load_value(p + k), inv), v1 = __fmul_rn(load_value(p + k + 1), inv);
-        q[(r * K + 32 * b + k) / 2] = static_cast<uint8_t>(c == 255u ? 0u : e2m1_pair(v0, v1));
-    }
-    sf[at] = static_cast<uint8_t>(c);
-}
-
-__global__ void __launch_bounds__(256) dequant_kernel(const uint8_t* q, const uint8_t* sf, int tiled, int64_t R,
-                                                      int64_t K, __nv_bfloat16* y) {
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int64_t nb = K / 32;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= R * nb) return;
-    const int64_t r = i / nb, b = i - r * nb;
-    const float s = e8m0_value(sf[tiled ? tiled_offset(r, b, K / 128) : i]);
-    for (int k = 0; k < 32; ++k) {
-        const uint8_t byte = q[(r * K + 32 * b + k) / 2];
-        y[r * K + 32 * b + k] = __float2bfloat16_rn(__fmul_rn(e2m1_value(k & 1 ? byte >> 4 : byte & 15u), s));
-    }
-}
-
-// One warp per output.
-__global__ void __launch_bounds__(256) gemm_kernel(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb,
-                                                   const uint8_t* sfb, int N, int K, int64_t m0, __nv_bfloat16* y) {
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int lane = threadIdx.x % 32;
-    const int n = blockIdx.x * 8 + threadIdx.x / 32;
-    const int64_t m = m0 + blockIdx.y;
-    if (n >= N) return;
-    float acc = 0.0f;
-    for (int j = lane; j < K / 2; j += 32) {
-        const uint32_t a = qa[m * (K / 2) + j], b = qb[static_cast<int64_t>(n) * (K / 2) + j];
-        const float s = e8m0_value(sfa[tiled_offset(m, j / 16, K / 128)]) * e8m0_value(sfb[tiled_offset(n, j / 16, K / 128)]);
-        acc = fmaf(e2m1_value(a & 15u) * e2m1_value(b & 15u) + e2m1_value(a >> 4) * e2m1_value(b >> 4), s, acc);
-    }
+    __device__ __forceinline__ void get(float (&v)[16]) const {
+        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, o);
-    if (lane == 0) y[m * N + n] = __float2bfloat16_rn(acc);
+        for (int i = 0; i < 8; ++i) {
+            v[2 * i] = bf16_lo(u[i]);
+            v[2 * i + 1] = bf16_hi(u[i]);
+        }
+    }
+};
+template <>
+struct Half<float> {
+    float4 w[4];
+    __device__ __forceinline__ void load(const float* p) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+    }
+    __device__ __forceinline__ void get(float (&v)[16]) const {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[4 * i] = w[i].x, v[4 * i + 1] = w[i].y, v[4 * i + 2] = w[i].z, v[4 * i + 3] = w[i].w;
+    }
+};
+
+// Two binary32 values -> their E2M1 codes (nearest even, saturating; lo in
+// bits 0..3) in every byte.
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tmov.b32 %0, {b, b, b, b};\n\t}"
+        : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+// Eight values -> eight codes, v[0] in bits 0..3. The four bytes are joined
+// with byte permutations: one mov of four different .b8 registers came out
+// with three of them zero here (CUDA 12.9).
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+    const uint32_t lo = __byte_perm(e2m1x2(v[0], v[1]), e2m1x2(v[2], v[3]), 0x4040);
+    const uint32_t hi = __byte_perm(e2m1x2(v[4], v[5]), e2m1x2(v[6], v[7]), 0x4040);
+    return __byte_perm(lo, hi, 0x5410);
+}
+// Eight E2M1 codes times an FP32 scale -> eight BF16 values.
+__device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, float s) {
+    uint32_t h[4], o[4];
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(w));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+        o[i] = pack_bf16x2(__fmul_rn(f.x, s), __fmul_rn(f.y, s));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+constexpr int THREADS = 256;
+constexpr int BATCH = 4;   // halves of a lane in flight: 128 bytes of BF16
+
+// n / d for d > 0 with inv = floor((2^32 - 1) / d), n < 2^32: at most one short.
+__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t d, uint32_t inv, uint32_t& rest) {
+    uint32_t q = __umulhi(n, inv);
+    rest = n - q * d;
+    if (rest >= d) ++q, rest -= d;
+    return q;
+}
+
+struct RowArgs {
+    const void* x;       // quant: rows of ldx elements; dequant: null
+    uint8_t* q;          // [R, K / 2]
+    uint8_t* sf;
+    __nv_bfloat16* y;    // dequant: [R, K]
+    int64_t ldx;
+    uint32_t R, halves, inv;  // rows, halves per row (K / 16), for divide()
+    int64_t total;            // halves of all rows (quant, tiled: with the pad rows)
+    int tiled, groups;        // tiled scales; K a multiple of 128
+};
+
+// Scale byte offset of half h of row r.
+__device__ __forceinline__ int64_t scale_offset(const RowArgs& a, uint32_t r, uint32_t h) {
+    return a.tiled ? tiled_offset(r, h >> 1, a.halves >> 3) : static_cast<int64_t>(r) * (a.halves >> 1) + (h >> 1);
+}
+
+// A lane quantizes one half at a time. HBM-bound: 2 bytes read and 17/32
+// written per BF16 element; a warp reads 1 KB and writes 256 + 16 bytes of
+// consecutive memory per step, BATCH steps in flight.
+template <typename T>
+__global__ void __launch_bounds__(THREADS) quant_kernel(const RowArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * THREADS;
+    const int lane = threadIdx.x % 32;
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i0 - lane < a.total; i0 += BATCH * stride) {
+        Half<T> x[BATCH];
+        uint32_t r[BATCH], h[BATCH];
+        bool live[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int64_t i = i0 + b * stride;
+            const bool in = i < a.total;
+            r[b] = divide(static_cast<uint32_t>(in ? i : 0), a.halves, a.inv, h[b]);
+            live[b] = in && r[b] < a.R;
+            if (live[b]) x[b].load(static_cast<const T*>(a.x) + r[b] * a.ldx + 16 * h[b]);
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            float v[16];
+            uint32_t m = 0;
+            if (live[b]) {
+                x[b].get(v);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) m = max(m, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+            }
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));  // the block's other half
+            uint32_t c = live[b] ? scale_code(m) : 0u;       // the pad rows' scales are 0
+            if (live[b]) {
+                const float inv = __uint_as_float((254u - c) << 23);  // 2^(127 - c)
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __fmul_rn(v[k], inv);
+                uint2 o = make_uint2(e2m1x8(v), e2m1x8(v + 8));
+                if (c == 255u) o = make_uint2(0, 0);
+                *reinterpret_cast<uint2*>(a.q + (static_cast<int64_t>(r[b]) * a.halves + h[b]) * 8) = o;
+            }
+            const bool in = i0 + b * stride < a.total;
+            if (a.groups) {
+                // four blocks' scales in one word: lanes 0, 2, 4, 6 of each eight
+                c |= __shfl_down_sync(0xffffffffu, c, 2) << 8;
+                c |= __shfl_down_sync(0xffffffffu, c, 4) << 16;
+                if (in && (lane & 7) == 0) *reinterpret_cast<uint32_t*>(a.sf + scale_offset(a, r[b], h[b])) = c;
+            } else if (in && (lane & 1) == 0) {
+                a.sf[scale_offset(a, r[b], h[b])] = static_cast<uint8_t>(c);
+            }
+        }
+    }
+}
+
+// A lane reads back one half: 8.5 bytes read and 32 written.
+__global__ void __launch_bounds__(THREADS) dequant_kernel(const RowArgs a) {
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * THREADS;
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i0 < a.total; i0 += BATCH * stride) {
+        uint2 q[BATCH];
+        uint32_t c[BATCH];
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int64_t i = i0 + b * stride;
+            if (i < a.total) {
+                uint32_t h;
+                const uint32_t r = divide(static_cast<uint32_t>(i), a.halves, a.inv, h);
+                q[b] = *reinterpret_cast<const uint2*>(a.q + i * 8);
+                c[b] = a.sf[scale_offset(a, r, h)];
+            }
+        }
+#pragma unroll
+        for (int b = 0; b < BATCH; ++b) {
+            const int64_t i = i0 + b * stride;
+            if (i < a.total) {
+                const float s = e8m0_value(c[b]);
+                uint4* y = reinterpret_cast<uint4*>(a.y) + 2 * i;
+                y[0] = e2m1x8_to_bf16(q[b].x, s);
+                y[1] = e2m1x8_to_bf16(q[b].y, s);
+            }
+        }
+    }
 }
 
 int check_rows(const char* name, int64_t R, int64_t K, int layout) {
@@ -108,6 +208,33 @@ int check_rows(const char* name, int64_t R, int64_t K, int layout) {
         return fail(METIS_ERR_INVALID_ARG,
                     "%s: need R >= 0, 32 <= K <= 65536 with K %% 32 == 0 (tiled scales: K %% 128 == 0) "
                     "(R=%lld K=%lld)", name, (long long)R, (long long)K);
+    return METIS_OK;
+}
+
+// Rows per launch: divide() takes fewer than 2^32 halves. Whole 128-row atoms.
+constexpr int64_t MAX_HALVES = 0xF0000000ll;
+
+// Calls launch(rows' arguments, blocks) for consecutive parts of the rows.
+template <typename F>
+int by_parts(const DeviceInfo& di, RowArgs a, int64_t R, int64_t rows, int64_t K, int64_t x_bytes, F&& launch) {
+    a.halves = static_cast<uint32_t>(K / 16);
+    a.inv = 0xFFFFFFFFu / a.halves;
+    const int64_t part = MAX_HALVES / a.halves / 128 * 128;
+    for (int64_t r0 = 0; r0 < rows; r0 += part) {
+        const int64_t n = rows - r0 < part ? rows - r0 : part;
+        RowArgs b = a;
+        b.R = static_cast<uint32_t>(R - r0 < n ? (R > r0 ? R - r0 : 0) : n);
+        b.total = n * b.halves;
+        if (b.x) b.x = static_cast<const uint8_t*>(b.x) + r0 * b.ldx * x_bytes;
+        b.q += r0 * (K / 2);
+        b.sf += r0 * (K / 32);
+        if (b.y) b.y += r0 * K;
+        // at most 8 blocks of 256 threads per SM, each thread with BATCH halves in flight
+        int64_t blocks = (b.total + THREADS * BATCH - 1) / (THREADS * BATCH);
+        if (blocks < di.num_sms) blocks = (b.total + THREADS - 1) / THREADS;
+        if (blocks > 8ll * di.num_sms) blocks = 8ll * di.num_sms;
+        if (int rc = launch(b, static_cast<unsigned>(blocks))) return rc;
+    }
     return METIS_OK;
 }
 
@@ -135,15 +262,19 @@ extern "C" int metis_quant_mxfp4(const void* x, int x_kind, int64_t R, int64_t K
     DeviceInfo di;
     if ((rc = current_device_info(&di))) return rc;
     const int64_t rows = tiled ? (R + 127) / 128 * 128 : R;
-    const unsigned grid = static_cast<unsigned>((rows * (K / 32) + 255) / 256);
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (x_kind == METIS_A_BF16)
-        return cuda_check(launch_pdl(quant_kernel<__nv_bfloat16>, dim3(grid), dim3(256), 0, st, 1,
-                                     static_cast<const __nv_bfloat16*>(x), R, K, ldx, q, sf, tiled, rows),
+    RowArgs a{};
+    a.x = x;
+    a.q = q;
+    a.sf = sf;
+    a.ldx = ldx;
+    a.tiled = tiled;
+    a.groups = K % 128 == 0 && aligned(sf, 4);
+    const bool bf16 = x_kind == METIS_A_BF16;
+    return by_parts(di, a, R, rows, K, bf16 ? 2 : 4, [&](const RowArgs& b, unsigned blocks) {
+        return cuda_check(launch_pdl(bf16 ? quant_kernel<__nv_bfloat16> : quant_kernel<float>, dim3(blocks), dim3(THREADS),
+                                     0, static_cast<cudaStream_t>(stream), 1, b),
                           "quant_mxfp4 launch");
-    return cuda_check(launch_pdl(quant_kernel<float>, dim3(grid), dim3(256), 0, st, 1, static_cast<const float*>(x), R,
-                                 K, ldx, q, sf, tiled, rows),
-                      "quant_mxfp4 launch");
+    });
 }
 
 extern "C" int metis_dequant_mxfp4(const uint8_t* q, const uint8_t* sf, int sf_layout, int64_t R, int64_t K,
@@ -158,10 +289,15 @@ extern "C" int metis_dequant_mxfp4(const uint8_t* q, const uint8_t* sf, int sf_l
         return fail(METIS_ERR_INVALID_ARG, "dequant_mxfp4: q and y 16-byte aligned, tiled sf 4-byte aligned");
     DeviceInfo di;
     if ((rc = current_device_info(&di))) return rc;
-    const unsigned grid = static_cast<unsigned>((R * (K / 32) + 255) / 256);
-    return cuda_check(launch_pdl(dequant_kernel, dim3(grid), dim3(256), 0, static_cast<cudaStream_t>(stream), 1, q, sf,
-                                 tiled, R, K, static_cast<__nv_bfloat16*>(y_bf16)),
-                      "dequant_mxfp4 launch");
+    RowArgs a{};
+    a.q = const_cast<uint8_t*>(q);
+    a.sf = const_cast<uint8_t*>(sf);
+    a.y = static_cast<__nv_bfloat16*>(y_bf16);
+    a.tiled = tiled;
+    return by_parts(di, a, R, R, K, 0, [&](const RowArgs& b, unsigned blocks) {
+        return cuda_check(launch_pdl(dequant_kernel, dim3(blocks), dim3(THREADS), 0, static_cast<cudaStream_t>(stream), 1, b),
+                          "dequant_mxfp4 launch");
+    });
 }
 
 extern "C" int metis_mxfp4_gemm(const uint8_t* qa, const uint8_t* sfa, const uint8_t* qb, const uint8_t* sfb,
@@ -176,16 +312,7 @@ extern "C" int metis_mxfp4_gemm(const uint8_t* qa, const uint8_t* sfa, const uin
     if (!qa || !sfa || !qb || !sfb || !y_bf16) return fail(METIS_ERR_INVALID_ARG, "mxfp4_gemm: null pointer");
     if (!aligned(qa, 16) || !aligned(sfa, 16) || !aligned(qb, 16) || !aligned(sfb, 16) || !aligned(y_bf16, 16))
         return fail(METIS_ERR_INVALID_ARG, "mxfp4_gemm: codes, tiled scales and y 16-byte aligned");
-    DeviceInfo di;
-    int rc = current_device_info(&di);
-    if (rc) return rc;
-    for (int64_t m = 0; m < M; m += 65535) {
-        const unsigned rows = static_cast<unsigned>(M - m < 65535 ? M - m : 65535);
-        rc = cuda_check(launch_pdl(gemm_kernel, dim3(static_cast<unsigned>((N + 7) / 8), rows), dim3(256), 0,
-                                   static_cast<cudaStream_t>(stream), 1, qa, sfa, qb, sfb, static_cast<int>(N),
-                                   static_cast<int>(K), m, static_cast<__nv_bfloat16*>(y_bf16)),
-                        "mxfp4_gemm launch");
-        if (rc) return rc;
-    }
-    return METIS_OK;
+    return launch_mxfp4_gemm(qa, sfa, (M + 127) / 128 * 128, qb, sfb, N, static_cast<__nv_bfloat16*>(y_bf16),
+                             static_cast<int>(M), static_cast<int>(N), static_cast<int>(K),
+                             static_cast<cudaStream_t>(stream));
 }

@@ -39,6 +39,11 @@
 //                        buffers need columns too, so two accumulators do not
 //                        fit in 512). Dense tiles run in groups of RASTER_M row
 //                        blocks; grouped tiles follow the padded expert offsets.
+//                        With MX the dense kernel multiplies MXFP4 matrices
+//                        (kind::mxf4 block32: an E8M0 scale per 32 elements, so
+//                        one scale atom holds 128 elements and serves two MMAs,
+//                        which take the lower and the upper two of its four
+//                        scales; no global scales).
 #include "common.cuh"
 #include "../../include/metis_nvfp4.h"
 
@@ -487,8 +492,14 @@ constexpr int SCALE_WARP = 2 + EPI_WARPS;   // first of the warps copying scale 
 constexpr int SCALE_WARPS = 4;              // each copies one of a k-block's four 64-element chunks
 constexpr int THREADS = 64 + EPI_WARPS * 32 + SCALE_WARPS * 32;
 constexpr int ATOM = 512;       // one tiled scale atom: 128 rows x 4 scales
-constexpr int SFA_STAGE = KCH * ATOM;       // this CTA's 128 rows of A
-constexpr int SFB_STAGE = 2 * KCH * ATOM;   // both 128-row halves of B (every CTA)
+// MMA chunks of 64 elements per scale atom, and atoms per k-block
+template <bool MX>
+struct Sf {
+    static constexpr int CPA = MX ? 2 : 1;
+    static constexpr int ATOMS = KCH / CPA;
+    static constexpr int A_STAGE = ATOMS * ATOM;       // this CTA's 128 rows of A
+    static constexpr int B_STAGE = 2 * ATOMS * ATOM;   // both 128-row halves of B (every CTA)
+};
 constexpr int STAGING = EPI_WARPS * 32 * 64;    // a 32 x 32 BF16 block per epilogue warp
 constexpr int MAX_GROUPS = 1024;
 constexpr int TMEM_COLS = 512;
@@ -504,11 +515,18 @@ __host__ __device__ constexpr uint32_t idesc_nvf4(int m, int n) {
            (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// The same for kind::mxf4: E8M0 scales (bit 23); chunk c of an atom takes the
+// scales from id 2 c on (B's id at bit 4, A's at bit 29).
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int c) {
+    return idesc_nvf4(m, n) | (1u << 23) | (static_cast<uint32_t>(2 * c) << 4) | (static_cast<uint32_t>(2 * c) << 29);
+}
+
 // Shared-memory layout of the one-CTA (CTAS = 1, 128 x 256 tiles) and the
 // CTA-pair (CTAS = 2, 256 x 256 tiles: each CTA holds 128 rows of A, 128 rows
 // of B and the scales of all 256 rows of B) kernels.
-template <int CTAS, bool GROUPED>
+template <int CTAS, bool GROUPED, bool MX = false>
 struct Lay {
+    static constexpr int SFA_STAGE = Sf<MX>::A_STAGE, SFB_STAGE = Sf<MX>::B_STAGE;
     static constexpr int B_ROWS = BN / CTAS;
     static constexpr int A_STAGE = ROWS * BKB;
     static constexpr int B_STAGE = B_ROWS * BKB;
@@ -526,7 +544,10 @@ struct Lay {
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int GROUP_OFF = MISC_OFF + 16;
     static constexpr size_t BYTES = 1024 + GROUP_OFF + (GROUPED ? 3 * (MAX_GROUPS + 1) * 4 : 0);
-    static constexpr uint32_t IDESC = idesc_nvf4(ROWS * CTAS, BN);
+    // chunk c of a k-block
+    static constexpr uint32_t idesc(int c) {
+        return MX ? idesc_mxf4(ROWS * CTAS, BN, c & 1) : idesc_nvf4(ROWS * CTAS, BN);
+    }
     // CTA pair: both CTAs' loads of a stage counted on the even CTA's barrier
     static constexpr uint32_t PAIR_TX = CTAS * (A_STAGE + B_STAGE + SFA_STAGE + SFB_STAGE);
 };
@@ -554,9 +575,18 @@ __device__ __forceinline__ void sf_copy_pair(uint32_t taddr, uint64_t sdesc) {
                  : "memory");
 }
 
+template <bool MX>
 __device__ __forceinline__ void mma_nvf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                          uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                          uint32_t accumulate) {
+    if constexpr (MX)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+            : "memory");
+    else
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -567,9 +597,18 @@ __device__ __forceinline__ void mma_nvf4(uint32_t d_tmem, uint64_t adesc, uint64
 // The CTA pair's block-scaled MMA (M = 256: 128 rows of A per CTA, B rows
 // split between the CTAs, each CTA's TMEM holding its own rows of D, its own
 // A scales and all of B's scales).
+template <bool MX>
 __device__ __forceinline__ void mma_nvf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
                                               uint32_t idesc, uint32_t sfa, uint32_t sfb,
                                               uint32_t accumulate) {
+    if constexpr (MX)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "setp.ne.b32 p, %4, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.block32 [%0], %1, %2, %3, [%5], [%6], p;\n\t}"
+            ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb)
+            : "memory");
+    else
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
@@ -700,13 +739,14 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&v)[32], int c, cons
     }
 }
 
-template <int CTAS, bool GROUPED>
+template <int CTAS, bool GROUPED, bool MX = false>
 __global__ void __launch_bounds__(THREADS, 1)
 nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
                   const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
-    using L = Lay<CTAS, GROUPED>;
-    constexpr int STAGES = L::STAGES;
+    using L = Lay<CTAS, GROUPED, MX>;
+    constexpr int STAGES = L::STAGES, SFA_STAGE = L::SFA_STAGE, SFB_STAGE = L::SFB_STAGE;
+    constexpr int CPA = Sf<MX>::CPA, ATOMS = Sf<MX>::ATOMS;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = align1024(smem_raw);
     uint8_t* staging = smem + L::TILES;
@@ -830,6 +870,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const uint32_t tmem_base = *tmem_slot;
     const int kch_total = p.K / 64;             // 64-element chunks per row
     const int num_kb = (kch_total + KCH - 1) / KCH;
+    const int atoms_total = kch_total / CPA;    // scale atoms per 128 rows
     const int first = CTAS == 2 ? static_cast<int>(blockIdx.x / 2) : static_cast<int>(blockIdx.x);
     const int stride = CTAS == 2 ? static_cast<int>(gridDim.x / 2) : static_cast<int>(gridDim.x);
 
@@ -852,7 +893,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         *abort_flag = 1;
                         break;
                     }
-                    const int64_t c0 = static_cast<int64_t>(kb) * KCH;
+                    const int64_t c0 = static_cast<int64_t>(kb) * ATOMS;
                     const uint32_t sa = smem_u32(smem + L::A_OFF + stage * L::A_STAGE);
                     const uint32_t sb = smem_u32(smem + L::B_OFF + stage * L::B_STAGE);
                     const uint32_t ssa = smem_u32(smem + L::SFA_OFF + stage * SFA_STAGE);
@@ -865,19 +906,19 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         if (leader) mbar_arrive_expect_tx(landed(stage), L::PAIR_TX);
                         tma_load_2d_pair(sa, &tmA, kb * BKB, ti.a_row0, fl);
                         tma_load_2d_pair(sb, &tmB, kb * BKB, ti.b_row0, fl);
-                        tma_load_2d_pair(ssa, &tmSFA, 0, static_cast<int32_t>((rb_a * kch_total + c0) * RPA), fl);
-                        tma_load_2d_pair(ssb, &tmSFB, 0, static_cast<int32_t>((rb_b0 * kch_total + c0) * RPA), fl);
-                        tma_load_2d_pair(ssb + KCH * ATOM, &tmSFB, 0,
-                                         static_cast<int32_t>((rb_b1 * kch_total + c0) * RPA), fl);
+                        tma_load_2d_pair(ssa, &tmSFA, 0, static_cast<int32_t>((rb_a * atoms_total + c0) * RPA), fl);
+                        tma_load_2d_pair(ssb, &tmSFB, 0, static_cast<int32_t>((rb_b0 * atoms_total + c0) * RPA), fl);
+                        tma_load_2d_pair(ssb + ATOMS * ATOM, &tmSFB, 0,
+                                         static_cast<int32_t>((rb_b1 * atoms_total + c0) * RPA), fl);
                     } else {
                         const int nk = min(KCH, kch_total - kb * KCH);
-                        const uint32_t sfb = static_cast<uint32_t>(nk * ATOM);
+                        const uint32_t sfb = static_cast<uint32_t>(nk / CPA * ATOM);
                         mbar_arrive_expect_tx(landed(stage), L::A_STAGE + L::B_STAGE + 3 * sfb);
                         tma_load_2d(sa, &tmA, kb * BKB, ti.a_row0, landed(stage));
                         tma_load_2d(sb, &tmB, kb * BKB, ti.b_row0, landed(stage));
-                        bulk_load(ssa, p.sfa + (rb_a * kch_total + c0) * ATOM, sfb, landed(stage));
-                        bulk_load(ssb, p.sfb + (rb_b0 * kch_total + c0) * ATOM, sfb, landed(stage));
-                        bulk_load(ssb + KCH * ATOM, p.sfb + (rb_b1 * kch_total + c0) * ATOM, sfb, landed(stage));
+                        bulk_load(ssa, p.sfa + (rb_a * atoms_total + c0) * ATOM, sfb, landed(stage));
+                        bulk_load(ssb, p.sfb + (rb_b0 * atoms_total + c0) * ATOM, sfb, landed(stage));
+                        bulk_load(ssb + ATOMS * ATOM, p.sfb + (rb_b1 * atoms_total + c0) * ATOM, sfb, landed(stage));
                     }
                     issued |= 1u << stage;
                     issued_phase = (issued_phase & ~(1u << stage)) | (phase << stage);
@@ -928,11 +969,11 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                         if (c < nk) {
                             const uint32_t acc = (kb > 0 || c > 0) ? 1u : 0u;
                             if constexpr (CTAS == 2)
-                                mma_nvf4_pair(tmem_base, adesc + 2 * c, bdesc + 2 * c, L::IDESC, sfa_t + 4 * c,
-                                              sfb_t + 8 * c, acc);
+                                mma_nvf4_pair<MX>(tmem_base, adesc + 2 * c, bdesc + 2 * c, L::idesc(c),
+                                                  sfa_t + 4 * (c / CPA), sfb_t + 8 * (c / CPA), acc);
                             else
-                                mma_nvf4(tmem_base, adesc + 2 * c, bdesc + 2 * c, L::IDESC, sfa_t + 4 * c,
-                                         sfb_t + 8 * c, acc);
+                                mma_nvf4<MX>(tmem_base, adesc + 2 * c, bdesc + 2 * c, L::idesc(c),
+                                             sfa_t + 4 * (c / CPA), sfb_t + 8 * (c / CPA), acc);
                         }
                     }
                     if constexpr (CTAS == 2) mma_commit_pair_mc(empty(stage), 0x3);
@@ -956,7 +997,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             mbar_wait(drain, 0, p.timeout_ns, p.status);
         }
     } else if (warp >= SCALE_WARP) {
-        const int part = warp - SCALE_WARP;   // chunks [part * KCH / SCALE_WARPS, ...)
+        const int part = warp - SCALE_WARP;   // the atom of a k-block that this warp copies (MX: two warps only commit)
         if (lane == 0 && leader) {
             // ------------------------------------------------- scale-factor copies
             // Each stage's scale atoms go into the stage's TMEM scale buffer as
@@ -979,16 +1020,16 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                     const uint32_t sa = smem_u32(smem + L::SFA_OFF + stage * SFA_STAGE);
                     const uint32_t sb = smem_u32(smem + L::SFB_OFF + stage * SFB_STAGE);
 #pragma unroll
-                    for (int c = 0; c < KCH; ++c) {
-                        if (c < nk && c / (KCH / SCALE_WARPS) == part) {
+                    for (int c = 0; c < ATOMS; ++c) {
+                        if (c * CPA < nk && c == part) {
                             if constexpr (CTAS == 2) {
                                 sf_copy_pair(sfa_t + 4 * c, sf_atom_desc(sa + c * ATOM));
                                 sf_copy_pair(sfb_t + 8 * c, sf_atom_desc(sb + c * ATOM));
-                                sf_copy_pair(sfb_t + 8 * c + 4, sf_atom_desc(sb + (KCH + c) * ATOM));
+                                sf_copy_pair(sfb_t + 8 * c + 4, sf_atom_desc(sb + (ATOMS + c) * ATOM));
                             } else {
                                 sf_copy(sfa_t + 4 * c, sf_atom_desc(sa + c * ATOM));
                                 sf_copy(sfb_t + 8 * c, sf_atom_desc(sb + c * ATOM));
-                                sf_copy(sfb_t + 8 * c + 4, sf_atom_desc(sb + (KCH + c) * ATOM));
+                                sf_copy(sfb_t + 8 * c + 4, sf_atom_desc(sb + (ATOMS + c) * ATOM));
                             }
                         }
                     }
@@ -1015,8 +1056,8 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
         for (int t = first; t < sc.total && !*abort_flag; t += stride) {
             const Tile ti = sc.get(t);
             const int row = ti.a_row0 + q * 32 + lane;
-            const float ga = row < ti.row_end ? p.ga[row] : 0.0f;
-            const float gb = p.gb[ti.group];
+            const float ga = MX ? 1.0f : row < ti.row_end ? p.ga[row] : 0.0f;
+            const float gb = MX ? 1.0f : p.gb[ti.group];
             if (!mbar_wait(tfull, acc_phase, p.timeout_ns, p.status)) {
                 *abort_flag = 1;
                 break;
@@ -1055,14 +1096,14 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     }
 }
 
-template <int CTAS, bool GROUPED>
+template <int CTAS, bool GROUPED, bool MX = false>
 int prepare_gemm(const DeviceInfo& di) {
     static std::atomic<uint64_t> done[64];
-    const size_t smem = Lay<CTAS, GROUPED>::BYTES;
+    const size_t smem = Lay<CTAS, GROUPED, MX>::BYTES;
     if (static_cast<size_t>(di.max_smem_optin) < smem)
         return fail(METIS_ERR_UNSUPPORTED, "nvfp4 gemm needs %zu bytes of shared memory", smem);
     return once_per_context(done, di.device, [&] {
-        return cuda_check(cudaFuncSetAttribute(nvfp4_gemm_kernel<CTAS, GROUPED>,
+        return cuda_check(cudaFuncSetAttribute(nvfp4_gemm_kernel<CTAS, GROUPED, MX>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem)),
                           "cudaFuncSetAttribute(nvfp4 gemm)");
@@ -1070,14 +1111,14 @@ int prepare_gemm(const DeviceInfo& di) {
 }
 
 // Co-resident CTA pairs of the 2-CTA kernel (cached per device).
-template <bool GROUPED>
+template <bool GROUPED, bool MX = false>
 int max_pairs(const DeviceInfo& di, int* out) {
     static int cached[64];
     if (!cached[di.device]) {
         cudaLaunchConfig_t cfg = {};
         cfg.gridDim = dim3(2 * (di.num_sms / 2), 1, 1);
         cfg.blockDim = dim3(THREADS, 1, 1);
-        cfg.dynamicSmemBytes = Lay<2, GROUPED>::BYTES;
+        cfg.dynamicSmemBytes = Lay<2, GROUPED, MX>::BYTES;
         cudaLaunchAttribute attr[1];
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
@@ -1086,7 +1127,7 @@ int max_pairs(const DeviceInfo& di, int* out) {
         cfg.attrs = attr;
         cfg.numAttrs = 1;
         int n = 0;
-        int rc = cuda_check(cudaOccupancyMaxActiveClusters(&n, nvfp4_gemm_kernel<2, GROUPED>, &cfg),
+        int rc = cuda_check(cudaOccupancyMaxActiveClusters(&n, nvfp4_gemm_kernel<2, GROUPED, MX>, &cfg),
                             "cudaOccupancyMaxActiveClusters(nvfp4)");
         if (rc) return rc;
         if (n < 1) return fail(METIS_ERR_UNSUPPORTED, "no CTA pair of the nvfp4 gemm fits an SM pair");
@@ -1102,11 +1143,14 @@ int max_pairs(const DeviceInfo& di, int* out) {
 // b_rows: rows of B ([groups * N]). offsets/counts null: dense with M rows.
 // CTA pairs (256-row tiles) for the grouped GEMM and for M > 128.
 // Arguments validated by the caller.
-int launch_nvfp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* ga, int64_t a_rows,
-                      const uint8_t* qb, const uint8_t* sfb, const float* gb, int64_t b_rows,
-                      __nv_bfloat16* y, const int32_t* offsets, const int32_t* counts, int E, int M,
-                      int N, int K, cudaStream_t st) {
+template <bool MX>
+static int launch_fp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* ga, int64_t a_rows,
+                           const uint8_t* qb, const uint8_t* sfb, const float* gb, int64_t b_rows,
+                           __nv_bfloat16* y, const int32_t* offsets, const int32_t* counts, int E, int M,
+                           int N, int K, cudaStream_t st) {
     using namespace nvfp4;
+    constexpr int SF_BLOCK = MX ? 32 : 16;   // elements per scale
+    constexpr int BOX = Sf<MX>::ATOMS * ATOM / SF_ROW;
     DeviceInfo di;
     int rc = current_device_info(&di);
     if (rc) return rc;
@@ -1138,17 +1182,17 @@ int launch_nvfp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* ga, in
     if ((rc = make_tmap_2d(&tb, qb, 1, static_cast<uint64_t>(K / 2), static_cast<uint64_t>(b_rows),
                            static_cast<uint64_t>(K / 2), BKB, b_box, true)))
         return rc;
-    // the tiled scales as rows of 256 bytes (two per atom), 4 atoms per box
-    if ((rc = make_tmap_2d(&tsa, sfa, 1, SF_ROW, static_cast<uint64_t>(a_rows) * (K / 16) / SF_ROW, SF_ROW,
-                           SF_ROW, KCH * ATOM / SF_ROW, false)))
+    // the tiled scales as rows of 256 bytes (two per atom), a k-block's atoms per box
+    if ((rc = make_tmap_2d(&tsa, sfa, 1, SF_ROW, static_cast<uint64_t>(a_rows) * (K / SF_BLOCK) / SF_ROW, SF_ROW,
+                           SF_ROW, BOX, false)))
         return rc;
-    if ((rc = make_tmap_2d(&tsb, sfb, 1, SF_ROW, static_cast<uint64_t>(b_rows) * (K / 16) / SF_ROW, SF_ROW,
-                           SF_ROW, KCH * ATOM / SF_ROW, false)))
+    if ((rc = make_tmap_2d(&tsb, sfb, 1, SF_ROW, static_cast<uint64_t>(b_rows) * (K / SF_BLOCK) / SF_ROW, SF_ROW,
+                           SF_ROW, BOX, false)))
         return rc;
     if (pair) {
         int pairs = 0;
         int clusters = 0;
-        if (grouped) {
+        if constexpr (!MX) if (grouped) {
             if ((rc = prepare_gemm<2, true>(di))) return rc;
             if ((rc = max_pairs<true>(di, &pairs))) return rc;
             clusters = pairs;
@@ -1156,21 +1200,34 @@ int launch_nvfp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* ga, in
                                          Lay<2, true>::BYTES, st, 2, ta, tb, tsa, tsb, ty, p),
                               "nvfp4 grouped gemm (CTA pair) launch");
         }
-        if ((rc = prepare_gemm<2, false>(di))) return rc;
-        if ((rc = max_pairs<false>(di, &pairs))) return rc;
+        if ((rc = prepare_gemm<2, false, MX>(di))) return rc;
+        if ((rc = max_pairs<false, MX>(di, &pairs))) return rc;
         const int64_t tiles = ((static_cast<int64_t>(M) + 2 * ROWS - 1) / (2 * ROWS)) * ((N + BN - 1) / BN);
         clusters = static_cast<int>(tiles < pairs ? tiles : pairs);
-        return cuda_check(launch_pdl(nvfp4_gemm_kernel<2, false>, dim3(2 * clusters), dim3(THREADS),
-                                     Lay<2, false>::BYTES, st, 2, ta, tb, tsa, tsb, ty, p),
+        return cuda_check(launch_pdl(nvfp4_gemm_kernel<2, false, MX>, dim3(2 * clusters), dim3(THREADS),
+                                     Lay<2, false, MX>::BYTES, st, 2, ta, tb, tsa, tsb, ty, p),
                           "nvfp4 gemm (CTA pair) launch");
     }
     const int64_t tiles = ((static_cast<int64_t>(M) + ROWS - 1) / ROWS) * ((N + BN - 1) / BN);
     if (tiles == 0) return METIS_OK;
     const int grid = static_cast<int>(tiles < di.num_sms ? tiles : di.num_sms);
-    if ((rc = prepare_gemm<1, false>(di))) return rc;
-    return cuda_check(launch_pdl(nvfp4_gemm_kernel<1, false>, dim3(grid), dim3(THREADS), Lay<1, false>::BYTES,
+    if ((rc = prepare_gemm<1, false, MX>(di))) return rc;
+    return cuda_check(launch_pdl(nvfp4_gemm_kernel<1, false, MX>, dim3(grid), dim3(THREADS), Lay<1, false, MX>::BYTES,
                                  st, 1, ta, tb, tsa, tsb, ty, p),
                       "nvfp4 gemm launch");
+}
+
+int launch_nvfp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* ga, int64_t a_rows,
+                      const uint8_t* qb, const uint8_t* sfb, const float* gb, int64_t b_rows,
+                      __nv_bfloat16* y, const int32_t* offsets, const int32_t* counts, int E, int M,
+                      int N, int K, cudaStream_t st) {
+    return launch_fp4_gemm<false>(qa, sfa, ga, a_rows, qb, sfb, gb, b_rows, y, offsets, counts, E, M, N, K, st);
+}
+
+// y [M, N] = product of two MXFP4 matrices (mxfp4.cu); arguments validated by the caller.
+int launch_mxfp4_gemm(const uint8_t* qa, const uint8_t* sfa, int64_t a_rows, const uint8_t* qb, const uint8_t* sfb,
+                      int64_t b_rows, __nv_bfloat16* y, int M, int N, int K, cudaStream_t st) {
+    return launch_fp4_gemm<true>(qa, sfa, nullptr, a_rows, qb, sfb, nullptr, b_rows, y, nullptr, nullptr, 1, M, N, K, st);
 }
 
 }  // namespace metis

@@ -133,20 +133,31 @@ def _check(name, rc):
     return rc
 
 
-def _dense(name, *tensors):
-    """The tensors' checks that the C entry point cannot make: CUDA tensors of
-    one device, the current one, with dense rows."""
+def _pointers(name, *tensors):
+    """Device addresses, after the checks that the C entry point cannot make:
+    CUDA tensors of one device, the current one, with dense rows."""
     device = torch.cuda.current_device()
+    found = []
     for t in tensors:
-        if not t.is_cuda or t.device.index != device:
-            raise ValueError(f"{name}: tensors must be on the current CUDA device ({device}), got {t.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: tensors must be contiguous")
+        if t.get_device() != device or not t.is_contiguous():
+            _need(name, t.get_device() == device,
+                  f"tensors must be on the current CUDA device ({device}), got {t.device}")
+            _need(name, False, "tensors must be contiguous")
+        found.append(t.data_ptr())
+    return found
 
 
 def _need(name, ok, what):
     if not ok:
         raise ValueError(f"{name}: {what}")
+
+
+def _stream(stream):
+    """The stream's handle; None: torch's current stream of the current device,
+    without making a Stream object of it."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _bytes(workspace):
@@ -325,23 +336,22 @@ def metis_moe_nvfp4_workspace_offset(region, T, topk, E, H, I):
 
 # ------------------------------------------- default maths for few tokens
 
-def _moe_few(name, x, topk_ids, topk_w, up, down, codes_per_byte, y, workspace, act, stream):
+def _moe_few(name, x, topk_ids, topk_w, up, down, packed, y, workspace, act, stream):
     """The two few-token routed layers: shape checks and the call; `up` and
     `down` are (weights, scales...) as the C entry point takes them."""
     T, H = x.shape
-    topk = topk_ids.shape[1]
     E, I, hb = up[0].shape
-    _need(name, x.dtype == torch.bfloat16 and y.dtype == torch.bfloat16, "x and y must be torch.bfloat16")
+    slots = topk_ids.shape
+    _need(name, x.dtype == torch.bfloat16 == y.dtype, "x and y must be torch.bfloat16")
     _need(name, topk_ids.dtype == torch.int32 and topk_w.dtype == torch.float32,
           "topk_ids must be torch.int32 and topk_w torch.float32")
-    _need(name, topk_ids.shape == (T, topk) and topk_w.shape == (T, topk) and y.shape == (T, H),
+    _need(name, len(slots) == 2 and slots[0] == T and topk_w.shape == slots and y.shape == x.shape,
           "topk_ids, topk_w and y must match x")
-    _need(name, hb * codes_per_byte == H and down[0].shape == (E, H, I // codes_per_byte),
+    _need(name, hb * packed == H and down[0].shape == (E, H, I // packed),
           "w_up must be [E, I, H] and w_down [E, H, I]")
-    _dense(name, x, topk_ids, topk_w, *up, *down, y, workspace)
+    px, pi, pw, py, ws, *weights = _pointers(name, x, topk_ids, topk_w, y, workspace, *up, *down)
     return _check(name, getattr(load(), name)(
-        _p(x), _p(topk_ids), _p(topk_w), T, topk, E, H, I, *map(_p, up), *map(_p, down), int(act), _p(y),
-        _p(workspace), _bytes(workspace), _s(stream)))
+        px, pi, pw, T, slots[1], E, H, I, *weights, int(act), py, ws, _bytes(workspace), _stream(stream)))
 
 
 def metis_moe_w8a16(x, topk_ids, topk_w, w_up, s_up, w_down, s_down, y, workspace, act=METIS_ACT_NONE,
@@ -359,10 +369,10 @@ def metis_moe_nvfp4_w4a16(x, topk_ids, topk_w, w_up, sf_up, g_up, w_down, sf_dow
     """Routed-expert layer in the default maths with NVFP4 experts, for few
     tokens; weights and tiled scales as in :func:`metis_moe_nvfp4_grouped_gemm`."""
     name = "metis_moe_nvfp4_w4a16"
-    E, I, hb = w_up.shape
+    E = w_up.shape[0]
     _need(name, sf_up.numel() * 8 == w_up.numel() and sf_down.numel() * 8 == w_down.numel(),
           "sf_up and sf_down must hold one byte per 16 elements")
-    _need(name, g_up.numel() == E and g_down.numel() == E and g_up.dtype == g_down.dtype == torch.float32,
+    _need(name, g_up.numel() == E == g_down.numel() and g_up.dtype == g_down.dtype == torch.float32,
           "g_up and g_down must be FP32 [E]")
     return _moe_few(name, x, topk_ids, topk_w, (w_up, sf_up, g_up), (w_down, sf_down, g_down), 2, y, workspace,
                     act, stream)
@@ -374,13 +384,14 @@ def metis_nvfp4_w4a16_gemm(x, qb, sfb, gb, y, workspace=None, stream=None):
     name = "metis_nvfp4_w4a16_gemm"
     M, K = x.shape
     N = qb.shape[0]
-    _need(name, x.dtype == torch.bfloat16 and y.dtype == torch.bfloat16, "x and y must be torch.bfloat16")
+    _need(name, x.dtype == torch.bfloat16 == y.dtype, "x and y must be torch.bfloat16")
     _need(name, qb.shape == (N, K // 2) and y.shape == (M, N) and sfb.numel() * 16 >= (N + 127) // 128 * 128 * K,
           "qb must be [N, K/2], sfb its tiled scales and y [M, N]")
     _need(name, gb.numel() == 1 and gb.dtype == torch.float32, "gb must be one FP32 value")
-    _dense(name, x, qb, sfb, gb, y, *(() if workspace is None else (workspace,)))
+    px, pq, ps, pg, py = _pointers(name, x, qb, sfb, gb, y)
+    ws = None if workspace is None else _pointers(name, workspace)[0]
     return _check(name, load().metis_nvfp4_w4a16_gemm(
-        _p(x), _p(qb), _p(sfb), _p(gb), _p(y), M, N, K, _p(workspace), _bytes(workspace), _s(stream)))
+        px, pq, ps, pg, py, M, N, K, ws, _bytes(workspace), _stream(stream)))
 
 
 # ------------------------------------------------------------------ MXFP4
@@ -389,17 +400,18 @@ def metis_quant_mxfp4(x, q, sf, tiled=False, stream=None):
     """x [R, K] BF16 or FP32 -> q [R, K/2] packed E2M1 codes and sf E8M0 scales
     per 32 elements (row-major [R, K/32], or tiled). Rows of x may be strided."""
     name = "metis_quant_mxfp4"
-    R, K, ldx = _rows(x)
+    R, K = x.shape
+    ldx, step = x.stride()
     _need(name, x.dtype in (torch.bfloat16, torch.float32), "x must be torch.bfloat16 or torch.float32")
-    _need(name, x.stride(1) == 1 or K == 1, "the rows of x must be contiguous")
+    _need(name, step == 1 or K == 1, "the rows of x must be contiguous")
     rows = (R + 127) // 128 * 128 if tiled else R
     _need(name, q.numel() * 2 >= R * K and sf.numel() * 32 >= rows * K, "q or sf is too small")
-    _need(name, x.is_cuda and x.device == q.device, "tensors must be on one CUDA device")
-    _dense(name, q, sf)
+    pq, ps = _pointers(name, q, sf)
+    _need(name, x.get_device() == q.get_device(), "x must be on the current CUDA device")
     kind = METIS_A_F32 if x.dtype == torch.float32 else METIS_A_BF16
     return _check(name, load().metis_quant_mxfp4(
-        _p(x), kind, R, K, ldx if R > 1 else K, _p(q), _p(sf), METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR,
-        _s(stream)))
+        x.data_ptr(), kind, R, K, ldx if R > 1 else K, pq, ps, METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR,
+        _stream(stream)))
 
 
 def metis_dequant_mxfp4(q, sf, y, tiled=False, stream=None):
@@ -409,9 +421,9 @@ def metis_dequant_mxfp4(q, sf, y, tiled=False, stream=None):
     rows = (R + 127) // 128 * 128 if tiled else R
     _need(name, y.dtype == torch.bfloat16, "y must be torch.bfloat16")
     _need(name, q.numel() * 2 >= R * K and sf.numel() * 32 >= rows * K, "q or sf is too small")
-    _dense(name, q, sf, y)
+    pq, ps, py = _pointers(name, q, sf, y)
     return _check(name, load().metis_dequant_mxfp4(
-        _p(q), _p(sf), METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR, R, K, _p(y), _s(stream)))
+        pq, ps, METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR, R, K, py, _stream(stream)))
 
 
 def metis_mxfp4_gemm(qa, sfa, qb, sfb, y, stream=None):
@@ -426,8 +438,8 @@ def metis_mxfp4_gemm(qa, sfa, qb, sfb, y, stream=None):
           "qa must be [ceil(M/128) * 128, K/2] and qb [N, K/2]")
     _need(name, sfa.numel() * 32 >= rows * K and sfb.numel() * 32 >= (N + 127) // 128 * 128 * K,
           "sfa or sfb is too small")
-    _dense(name, qa, sfa, qb, sfb, y)
-    return _check(name, load().metis_mxfp4_gemm(_p(qa), _p(sfa), _p(qb), _p(sfb), _p(y), M, N, K, _s(stream)))
+    pa, psa, pb, psb, py = _pointers(name, qa, sfa, qb, sfb, y)
+    return _check(name, load().metis_mxfp4_gemm(pa, psa, pb, psb, py, M, N, K, _stream(stream)))
 
 
 # ------------------------------------------------------------ shared expert
