@@ -850,6 +850,54 @@ __global__ void __launch_bounds__(256) combine_kernel(const float* o, const int3
     y[static_cast<int64_t>(t) * H + n] = __float2bfloat16_rn(acc);
 }
 
+// NVFP4 weights [N, K] widened exactly to BF16, D2(q) D(sf) (six significant
+// bits), and the global scale repeated for every column of the product. One
+// lane per block of 16: 8.5 bytes read, 32 written (HBM-bound, mostly into L2).
+constexpr int WIDEN_BATCH = 4;
+__global__ void __launch_bounds__(256) widen_kernel(const uint8_t* __restrict__ q, const uint8_t* __restrict__ sf,
+                                                    const float* __restrict__ g, uint32_t blocks, uint32_t row_blocks,
+                                                    uint32_t inv, int N, uint4* __restrict__ out, float* __restrict__ col) {
+    // the workspace may still be read by the previous kernel
+    grid_dependency_wait();
+    grid_launch_dependents();
+    const uint32_t stride = gridDim.x * 256u, i0 = blockIdx.x * 256u + threadIdx.x;
+    for (uint32_t n = i0; n < static_cast<uint32_t>(N); n += stride) col[n] = *g;
+    for (uint64_t base = i0; base < blocks; base += static_cast<uint64_t>(WIDEN_BATCH) * stride) {
+        uint2 w[WIDEN_BATCH];
+        uint32_t c[WIDEN_BATCH];
+#pragma unroll
+        for (int u = 0; u < WIDEN_BATCH; ++u) {
+            const uint64_t i = base + static_cast<uint64_t>(u) * stride;
+            if (i < blocks) {
+                int b;
+                const uint32_t r = divide(static_cast<uint32_t>(i), row_blocks, inv, b);
+                w[u] = __ldg(reinterpret_cast<const uint2*>(q) + i);
+                c[u] = __ldg(sf + static_cast<uint64_t>((r >> 7) * (row_blocks >> 2) + (b >> 2)) * 512 + 16 * (r & 31) +
+                             4 * ((r & 127) >> 5) + (b & 3));
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < WIDEN_BATCH; ++u) {
+            const uint64_t i = base + static_cast<uint64_t>(u) * stride;
+            if (i >= blocks) continue;
+            uint32_t s, unused;
+            scale_pairs(c[u], s, unused);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t h[4], o[4];
+                e2m1x8_to_f16(k ? w[u].y : w[u].x, h);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t v = mul_f16x2(h[j], s);
+                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+                    o[j] = pack_bf16x2(f.x, f.y);
+                }
+                out[2 * i + k] = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+    }
+}
+
 inline int64_t align256(int64_t v) { return (v + 255) & ~static_cast<int64_t>(255); }
 
 // The argument checks that the two routed layers share (`step`: what H and I
@@ -960,6 +1008,13 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
 
 }  // namespace few
 
+// Most tokens for which metis_nvfp4_w4a16_gemm streams the weights.
+constexpr int64_t kStreamTokens = 64;
+
+size_t nvfp4_w4a16_workspace(int64_t M, int64_t N, int64_t K) {
+    return M <= kStreamTokens ? 0 : static_cast<size_t>(few::align256(2 * N * K) + few::align256(4 * N));
+}
+
 // Bytes of the routed layers' workspace: h [S, I] and o [S, H], FP32.
 size_t few_moe_workspace(int64_t T, int64_t topk, int64_t H, int64_t I) {
     return static_cast<size_t>(few::align256(4 * T * topk * I) + few::align256(4 * T * topk * H));
@@ -1043,6 +1098,25 @@ extern "C" int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, con
     DeviceInfo di;
     int rc = current_device_info(&di);
     if (rc) return rc;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (M > kStreamTokens) {
+        // many tokens: widen the weights once, then the BF16 CTA-pair GEMM
+        __nv_bfloat16* wide = static_cast<__nv_bfloat16*>(workspace);
+        float* col = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + few::align256(2 * N * K));
+        const int64_t blocks = N * K / 16;
+        if (blocks > 0xFFFFFFFFll)
+            return fail(METIS_ERR_UNSUPPORTED, "nvfp4_w4a16_gemm: N * K too large (N=%lld K=%lld)", (long long)N, (long long)K);
+        int64_t grid = (blocks + 256 * few::WIDEN_BATCH - 1) / (256 * few::WIDEN_BATCH);
+        if (grid > 8ll * di.num_sms) grid = 8ll * di.num_sms;
+        rc = cuda_check(launch_pdl(few::widen_kernel, dim3(static_cast<unsigned>(grid)), dim3(256), 0, st, 1, qb, sfb, gb,
+                                   static_cast<uint32_t>(blocks), static_cast<uint32_t>(K / 16),
+                                   0xFFFFFFFFu / static_cast<uint32_t>(K / 16), static_cast<int>(N),
+                                   reinterpret_cast<uint4*>(wide), col),
+                        "nvfp4 widening launch");
+        if (rc) return rc;
+        return launch_bf16_gemm(static_cast<const __nv_bfloat16*>(x_bf16), wide, static_cast<__nv_bfloat16*>(y_bf16),
+                                static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), col, st);
+    }
     few::Args a{};
     if ((rc = device_status_word(&a.status))) return rc;
     a.in = x_bf16;
@@ -1051,5 +1125,5 @@ extern "C" int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, con
     a.S = a.T = static_cast<int>(M);
     a.topk = 1;
     a.out = y_bf16;
-    return few::launch_few_by_size<few::NVFP4, few::DENSE>(di, a, a.S, N * K / 2, static_cast<cudaStream_t>(stream));
+    return few::launch_few_by_size<few::NVFP4, few::DENSE>(di, a, a.S, N * K / 2, st);
 }

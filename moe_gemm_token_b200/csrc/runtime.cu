@@ -282,6 +282,7 @@ int64_t moe4_region_offset(int region, int64_t T, int64_t topk, int64_t E, int64
 
 // few_tokens.cu
 size_t few_moe_workspace(int64_t T, int64_t topk, int64_t H, int64_t I);
+size_t nvfp4_w4a16_workspace(int64_t M, int64_t N, int64_t K);
 
 }  // namespace metis
 
@@ -377,6 +378,9 @@ extern "C" size_t metis_workspace_size(int op, int64_t M_or_T, int64_t N_or_I, i
         case METIS_OP_MOE_NVFP4_W4A16:
             if (topk < 1 || E < 1) return 0;
             return few_moe_workspace(M_or_T, topk, K_or_H, N_or_I);
+        case METIS_OP_NVFP4_W4A16:
+            // many tokens: the weights widened to BF16 [N, K], and one FP32 scale per column
+            return nvfp4_w4a16_workspace(M_or_T, N_or_I, K_or_H);
         default:
             return 0;
     }
