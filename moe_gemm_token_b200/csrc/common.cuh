@@ -79,6 +79,11 @@ int make_tmap_3d_u8(CUtensorMap* map, const void* base, uint64_t d0, uint64_t d1
 int launch_w8a16_tensor(const __nv_bfloat16* x, const uint8_t* wq, const float* s_w,
                         __nv_bfloat16* y, int M, int N, int K, cudaStream_t st);
 
+// NVFP4 weight-only GEMM on the tensor cores (w16_gemm.cu), weights widened
+// in the kernel; arguments validated by the caller.
+int launch_nvfp4_w4a16_tensor(const __nv_bfloat16* x, const uint8_t* q, const uint8_t* sf, const float* g,
+                              __nv_bfloat16* y, int M, int N, int K, cudaStream_t st);
+
 // Per-row E4M3 quantizer (quant.cu), for T = __nv_bfloat16 or float; the
 // arguments are validated by the caller. dst_rows non-null: row r's codes
 // and scale go to rows dst_rows[r * topk + j] (negative entries skipped).

@@ -26,17 +26,17 @@ struct Weights {
     int N, K;
 };
 
+enum Mode { UP = 0, DOWN = 1, OWN = 2, DENSE = 3 };
+
 // Geometry by warps per CTA: 8 warps leave room on an SM for a CTA of the next
 // kernel, whose prologue then overlaps (few weights per SM: latency); 16 take
 // an SM by themselves and share one staged operand (many weights per SM).
 // depth: pieces in flight per warp. 64 KB per SM cover the memory latency.
-template <int W>
+template <int W, int GMAX, int MODE>
 struct Cta {
-    static constexpr int THREADS = W * 32;
-    static constexpr int DEPTH = W == 8 ? 8 : 4;
+    // fewer pieces leave room for the operand: 16 rows of K = 4096 (DENSE)
+    static constexpr int DEPTH = W == 8 ? 8 : GMAX == 1 || (GMAX == 2 && MODE != DENSE) ? 4 : 3;
 };
-
-enum Mode { UP = 0, DOWN = 1, OWN = 2, DENSE = 3 };
 
 // Per-format geometry. A piece is 16 rows by 64 bytes: lane (g, t) = (lane / 4,
 // lane % 4) holds bytes 16 t .. 16 t + 15 of rows g and g + 8.
@@ -89,16 +89,16 @@ __device__ __forceinline__ int divide(uint32_t n, uint32_t d, uint32_t inv, int&
 struct Smem {
     int part, x, unshift, items, route, own, total;
 };
-template <int W>
-__host__ __device__ inline Smem smem_layout(int slot_bytes, int gmax, int P, int pitch, int E, int S, bool routed,
-                                            bool own) {
+template <int W, int GMAX, int MODE>
+__host__ __device__ inline Smem smem_layout(int slot_bytes, int P, int pitch, int E, int S) {
+    constexpr bool routed = MODE != DENSE, own = MODE == OWN;
     Smem s;
-    s.part = W * Cta<W>::DEPTH * slot_bytes;
-    s.x = s.part + (gmax == 1 ? 2 : 1) * W * 512 * gmax;
+    s.part = W * Cta<W, GMAX, MODE>::DEPTH * slot_bytes;
+    s.x = s.part + (GMAX == 1 ? 2 : 1) * W * 512 * GMAX;
     s.unshift = s.x + P * pitch;
     s.items = s.unshift + ((P * 8 + 15) & ~15);
     s.route = s.items + 2 * W * static_cast<int>(sizeof(Item));
-    s.own = s.route + (routed ? 4 * (E + 4 * S + 2) : 16);
+    s.own = s.route + (routed ? 4 * (E + 4 * S + 3) : 16);
     s.own = (s.own + 15) & ~15;
     s.total = s.own + (own ? S * 16 * 4 : 0);
     return s;
@@ -393,7 +393,7 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
     }
     __syncthreads();
     if (threadIdx.x < 32) {
-        int nj = 0, tot = 0;
+        int nj = 0, tot = 0, chosen = 0;
         for (int e0 = 0; e0 < a.E; e0 += 32) {
             const int c = e0 + lane < a.E ? count[e0 + lane] : 0;
             const int own = c | ((c + columns - 1) / columns) << 16;
@@ -402,14 +402,19 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
             if (c > 0) count[e0 + lane] = (tot + ((incl - own) & 0xFFFF)) | c << 16;  // first entry, slots
             const int all = __shfl_sync(0xffffffffu, incl, 31);
             nj += all >> 16;
+            chosen += __popc(__ballot_sync(0xffffffffu, c > 0));
             tot += all & 0xFFFF;
         }
         if (lane == 0) {
             r.start[nj] = tot;
-            *jobs = nj;
+            jobs[0] = nj;
+            jobs[1] = chosen;
         }
     }
     __syncthreads();
+    r.jobs = *jobs;
+    // an expert with several jobs: its slots in ascending order
+    if (r.jobs > jobs[1]) {
 #pragma unroll
     for (int i = 0; i < MAX_S / THREADS; ++i)
         if (id[i] >= 0) r.row[(count[id[i]] & 0xFFFF) + rank[i]] = threadIdx.x + i * THREADS;
@@ -426,6 +431,7 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
             }
         }
     __syncthreads();
+    }
 #pragma unroll
     for (int i = 0; i < MAX_S / THREADS; ++i)
         if (id[i] >= 0) {
@@ -433,7 +439,6 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
             r.slots[at] = s;
             r.row[at] = MODE == UP ? s / a.topk : s;
         }
-    r.jobs = *jobs;
     __syncthreads();
     return r;
 }
@@ -441,11 +446,11 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
 template <int FMT, int MODE, int GMAX, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args a) {
     using G = Geo<FMT>;
-    constexpr int THREADS = WARPS * 32, DEPTH = Cta<WARPS>::DEPTH;
+    constexpr int THREADS = WARPS * 32, DEPTH = Cta<WARPS, GMAX, MODE>::DEPTH;
     constexpr int LOG = WARPS == 8 ? 3 : 4;
     using In = typename std::conditional<MODE == UP || MODE == DENSE, __nv_bfloat16, float>::type;
     extern __shared__ __align__(128) uint8_t smem[];
-    const Smem L = smem_layout<WARPS>(G::SLOT, GMAX, a.P, a.pitch, a.E, a.S, MODE != DENSE, MODE == OWN);
+    const Smem L = smem_layout<WARPS, GMAX, MODE>(G::SLOT, a.P, a.pitch, a.E, a.S);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, t = lane & 3;
     const int N = a.w.N, K = a.w.K;
@@ -834,20 +839,46 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     }
 }
 
-// y[t] = bf16( sum_j w[t, j] o[t, j] ), FP32, j ascending; slots of no expert add nothing.
-__global__ void __launch_bounds__(256) combine_kernel(const float* o, const int32_t* ids, const float* tw, int topk,
-                                                      int E, int H, __nv_bfloat16* y) {
-    grid_launch_dependents();
-    grid_dependency_wait();
-    const int n = blockIdx.x * 256 + threadIdx.x;
+// y[t] = bf16( sum_j w[t, j] o[t, j] ), FP32, j ascending; slots of no expert
+// add nothing. A thread makes four columns of one token, COMBINE_U slots'
+// values in flight.
+constexpr int COMBINE_U = 8;
+__global__ void __launch_bounds__(128) combine_kernel(const float* __restrict__ o, const int32_t* __restrict__ ids,
+                                                      const float* __restrict__ tw, int topk, int E, int H,
+                                                      __nv_bfloat16* __restrict__ y) {
+    const int n = 4 * (blockIdx.x * 128 + threadIdx.x);
     const int t = blockIdx.y;
+    grid_dependency_wait();
+    grid_launch_dependents();
     if (n >= H) return;
-    float acc = 0.0f;
-    for (int j = 0; j < topk; ++j) {
-        const int s = t * topk + j;
-        if (ids[s] >= 0 && ids[s] < E) acc = fmaf(tw[s], o[static_cast<int64_t>(s) * H + n], acc);
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = 0; j0 < topk; j0 += COMBINE_U) {
+        float4 v[COMBINE_U];
+        float w[COMBINE_U];
+        bool in[COMBINE_U];
+#pragma unroll
+        for (int u = 0; u < COMBINE_U; ++u) {
+            const int s = t * topk + j0 + u;
+            in[u] = false;
+            if (j0 + u < topk) {
+                const int e = ids[s];
+                w[u] = tw[s];
+                // (an id of no expert: o was not written there, and is not used)
+                v[u] = *reinterpret_cast<const float4*>(o + static_cast<int64_t>(s) * H + n);
+                in[u] = e >= 0 && e < E;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < COMBINE_U; ++u)
+            if (in[u]) {
+                acc[0] = fmaf(w[u], v[u].x, acc[0]);
+                acc[1] = fmaf(w[u], v[u].y, acc[1]);
+                acc[2] = fmaf(w[u], v[u].z, acc[2]);
+                acc[3] = fmaf(w[u], v[u].w, acc[3]);
+            }
     }
-    y[static_cast<int64_t>(t) * H + n] = __float2bfloat16_rn(acc);
+    *reinterpret_cast<uint2*>(y + static_cast<int64_t>(t) * H + n) =
+        make_uint2(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]));
 }
 
 // NVFP4 weights [N, K] widened exactly to BF16, D2(q) D(sf) (six significant
@@ -933,7 +964,7 @@ int launch_few(const DeviceInfo& di, Args a, bool latency, cudaStream_t st) {
     if (rc) return rc;
     a.pitch = operand_pitch<FMT>(a.w.K);
     constexpr int HALF = 112 * 1024;  // two CTAs per SM
-    auto bytes = [&](int P) { return smem_layout<W>(G::SLOT, GMAX, P, a.pitch, a.E, a.S, MODE != DENSE, MODE == OWN).total; };
+    auto bytes = [&](int P) { return smem_layout<W, GMAX, MODE>(G::SLOT, P, a.pitch, a.E, a.S).total; };
     const int base = bytes(0) + 32;  // rounding
     const int half = (HALF - base) / (a.pitch + 8), full = (di.max_smem_optin - base) / (a.pitch + 8);
     const int per_job = a.T < 8 * GMAX ? a.T : 8 * GMAX;
@@ -965,8 +996,9 @@ int launch_few_by_size(const DeviceInfo& di, const Args& a, int columns, int64_t
     const bool long_rows = operand_pitch<FMT>(a.w.K) * 8 > 112 * 1024;
     if ((columns <= 8 && small) || long_rows) return launch_few<FMT, MODE, 1, 8>(di, a, true, st);
     if (columns <= 8) return launch_few<FMT, MODE, 1, 16>(di, a, false, st);
-    if (columns <= 16) return launch_few<FMT, MODE, 2, 16>(di, a, false, st);
-    return launch_few<FMT, MODE, 4, 16>(di, a, false, st);
+    if (columns <= 16 || MODE == DENSE) return launch_few<FMT, MODE, 2, 16>(di, a, false, st);
+    if constexpr (MODE != DENSE) return launch_few<FMT, MODE, 4, 16>(di, a, false, st);
+    return METIS_OK;
 }
 
 template <int FMT>
@@ -1001,18 +1033,27 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
     }
     a.out = o;
     if ((rc = launch_few_by_size<FMT, DOWN>(di, a, columns, weight_bytes, st))) return rc;
-    return cuda_check(launch_pdl(combine_kernel, dim3((down.N + 255) / 256, T), dim3(256), 0, st, 1,
+    return cuda_check(launch_pdl(combine_kernel, dim3((down.N + 511) / 512, T), dim3(128), 0, st, 1,
                                  static_cast<const float*>(o), ids, tw, topk, E, down.N, y),
                       "few-token combine launch");
 }
 
 }  // namespace few
 
-// Most tokens for which metis_nvfp4_w4a16_gemm streams the weights.
-constexpr int64_t kStreamTokens = 64;
+// metis_nvfp4_w4a16_gemm by its tokens, measured on B200 (us; N x K):
+//                        6144x2048   14336x4096   2048x8192
+//    16  stream              10.5        20.5        15.1
+//        tensor cores        12.8        22.2        38.3
+//    32  stream              21.6        52.5           -
+//        tensor cores        12.8        22.3        38.5
+//  2048  tensor cores        48.5           -           -
+//        widened first       50.7           -           -
+//  4096  tensor cores        92.2           -           -
+//        widened first       82.4           -           -
+constexpr int64_t kStreamTokens = 16, kWidenTokens = 2048;
 
 size_t nvfp4_w4a16_workspace(int64_t M, int64_t N, int64_t K) {
-    return M <= kStreamTokens ? 0 : static_cast<size_t>(few::align256(2 * N * K) + few::align256(4 * N));
+    return M <= kWidenTokens ? 0 : static_cast<size_t>(few::align256(2 * N * K) + few::align256(4 * N));
 }
 
 // Bytes of the routed layers' workspace: h [S, I] and o [S, H], FP32.
@@ -1099,7 +1140,11 @@ extern "C" int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, con
     int rc = current_device_info(&di);
     if (rc) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (M > kStreamTokens) {
+    if (M > kStreamTokens && M <= kWidenTokens)
+        return launch_nvfp4_w4a16_tensor(static_cast<const __nv_bfloat16*>(x_bf16), qb, sfb, gb,
+                                         static_cast<__nv_bfloat16*>(y_bf16), static_cast<int>(M), static_cast<int>(N),
+                                         static_cast<int>(K), st);
+    if (M > kWidenTokens) {
         // many tokens: widen the weights once, then the BF16 CTA-pair GEMM
         __nv_bfloat16* wide = static_cast<__nv_bfloat16*>(workspace);
         float* col = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + few::align256(2 * N * K));

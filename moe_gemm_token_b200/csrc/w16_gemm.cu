@@ -33,6 +33,12 @@
 // commits to one (which both the producer and the converters wait on), and
 // when there are tiles enough the 256-token tiles halve the MMAs per FLOP.
 // Every mbarrier wait is bounded by the device watchdog.
+//
+// With FP4 the weights are NVFP4 (launch_nvfp4_w4a16_tensor): a converter
+// thread reads 32 code bytes and one word of four block scales per stage, PF
+// = 8 stages ahead, and widens D2(q) D(sf) exactly (FP16 product, six
+// significant bits); the epilogue applies the one global scale. Tiles of 32
+// and 64 tokens keep the MMAs of few tokens short (N = 32 or 64).
 #include "common.cuh"
 
 namespace metis {
@@ -44,7 +50,9 @@ constexpr int TILE_N = 128;      // channels per tile (TMEM lanes)
 constexpr int A_COLS = BKE / 2;  // TMEM columns per weight stage (two BF16 per column)
 constexpr int TMEM_COLS = 512;
 constexpr int CONV_WARPS = 8;   // two per TMEM lane quadrant, each on half of a stage
-constexpr int PF = 4;           // stages of weight bytes in flight per converter thread
+// stages of weight bytes in flight per converter thread
+template <bool FP4>
+constexpr int pf() { return FP4 ? 8 : 4; }
 constexpr int THREADS = 64 + CONV_WARPS * 32 + 4 * 32;
 
 // Tiles of TM tokens (accumulator columns). TM = 128: two accumulators (the
@@ -54,8 +62,8 @@ constexpr int THREADS = 64 + CONV_WARPS * 32 + 4 * 32;
 // drain of a tile is not overlapped with the next tile's MMAs.
 template <int TM>
 struct Cfg {
-    static constexpr int ACCS = TM == 128 ? 2 : 1;
-    static constexpr int STAGES = TM == 128 ? 4 : 3;  // x ring and TMEM weight stages
+    static constexpr int ACCS = TM <= 128 ? 2 : 1;
+    static constexpr int STAGES = TM <= 128 ? 4 : 3;  // x ring and TMEM weight stages
     static constexpr int X_BOX = TM * BOXE * 2;       // 16 or 32 KB
     static constexpr int X_STAGE = 2 * X_BOX;
     static constexpr int A_COL0 = ACCS * TM;          // weight stages after the accumulators
@@ -67,13 +75,14 @@ struct Cfg {
     static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 1;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr size_t SMEM_BYTES = 1024 + MISC_OFF + 16;
-    static_assert(TM == 128 || TM == 256, "tile width");
+    static_assert(TM == 32 || TM == 64 || TM == 128 || TM == 256, "tile width");
     static_assert(A_COL0 + STAGES * A_COLS <= TMEM_COLS, "TMEM budget");
 };
 
 struct Params {
     const uint8_t* w;     // [N, K] E4M3
-    const float* s_w;     // [N]
+    const float* s_w;     // [N]; FP4: the one global scale
+    const uint8_t* sf;    // FP4: tiled block scales
     __nv_bfloat16* y;     // [M, N]
     int M, N, K;
     uint32_t* status;
@@ -119,10 +128,34 @@ __device__ __forceinline__ void e4m3x4_to_bf16x2x2(uint32_t w, uint32_t& lo, uin
         : "r"(w));
 }
 
-template <int TM>
+// Sixteen E2M1 codes (one block) times their E4M3 scale -> eight BF16 pairs,
+// exactly: the FP16 product has six significant bits and is at most 2688.
+__device__ __forceinline__ void nvfp4x16_to_bf16(uint32_t w0, uint32_t w1, uint32_t scale, uint32_t* out) {
+    uint32_t s;
+    asm("{\n\t.reg .b16 q;\n\tcvt.u16.u32 q, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, q;\n\t}" : "=r"(s) : "r"(scale & 0xFFu));
+    s = __byte_perm(s, s, 0x1010);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t h[4];
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+            "cvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+            : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(i ? w1 : w0));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t v;
+            asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(v) : "r"(h[j]), "r"(s));
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+            out[4 * i + j] = pack_bf16x2(f.x, f.y);
+        }
+    }
+}
+
+template <int TM, bool FP4 = false>
 __global__ void __launch_bounds__(THREADS, 1)
 w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
     using C = Cfg<TM>;
+    constexpr int PF = pf<FP4>();
     constexpr int STAGES = C::STAGES;
     constexpr int X_BOX = C::X_BOX;
     constexpr int X_STAGE = C::X_STAGE;
@@ -253,12 +286,34 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
         for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x) {
             const int row = (t / num_m) * TILE_N + lane_base + lane;  // weight row = output channel
             const bool row_ok = row < p.N;
-            const uint8_t* wrow = p.w + static_cast<size_t>(row_ok ? row : 0) * p.K + 64 * half;
+            const size_t row_bytes = FP4 ? p.K / 2 : p.K;
+            const uint8_t* wrow = p.w + static_cast<size_t>(row_ok ? row : 0) * row_bytes + (FP4 ? 32 : 64) * half;
+            // FP4: the row's scale word of chunk c is at 512 c
+            const uint8_t* srow = FP4 ? p.sf + static_cast<size_t>(row >> 7) * (p.K / 64) * 512 + 16 * (row & 31) +
+                                            4 * ((row & 127) >> 5)
+                                      : nullptr;
             // a thread's 64 bytes of a stage are two sectors: 32-byte loads
             // when the rows are 32-byte aligned (K % 32 == 0; two 16-byte
             // loads of the same sector would each move the whole sector
             // through L1), 16-byte loads otherwise and at the end of K
+            auto load_fp4 = [&](int kb, uint4 (&r)[4]) {
+                r[0] = r[1] = r[2] = make_uint4(0, 0, 0, 0);
+                if (row_ok && kb * BKE + 64 * half < p.K) {
+                    // one 32-byte load touches each of the warp's 32 rows once
+                    if (wide) {
+                        ld_w32(wrow + kb * (BKE / 2), r[0], r[1]);
+                    } else {
+                        r[0] = ld_w16(wrow + kb * (BKE / 2));
+                        r[1] = ld_w16(wrow + kb * (BKE / 2) + 16);
+                    }
+                    r[2].x = __ldg(reinterpret_cast<const uint32_t*>(srow + static_cast<size_t>(2 * kb + half) * 512));
+                }
+            };
             auto load_kb = [&](int kb, uint4 (&r)[4]) {
+                if constexpr (FP4) {
+                    load_fp4(kb, r);
+                    return;
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int k0 = kb * BKE + 64 * half + 32 * h;
@@ -285,6 +340,13 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
                     const int kb = kb0 + d;
                     if (kb >= num_kb || !ok) break;
                     uint32_t words[32];
+                    if constexpr (FP4) {
+                        const uint32_t sc = buf[d][2].x;
+                        nvfp4x16_to_bf16(buf[d][0].x, buf[d][0].y, sc, words);
+                        nvfp4x16_to_bf16(buf[d][0].z, buf[d][0].w, sc >> 8, words + 8);
+                        nvfp4x16_to_bf16(buf[d][1].x, buf[d][1].y, sc >> 16, words + 16);
+                        nvfp4x16_to_bf16(buf[d][1].z, buf[d][1].w, sc >> 24, words + 24);
+                    } else
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const uint32_t v[4] = {buf[d][j].x, buf[d][j].y, buf[d][j].z, buf[d][j].w};
@@ -322,7 +384,7 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
         for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x) {
             const int m0 = (t % num_m) * TM;
             const int n_lane = (t / num_m) * TILE_N + q * 32 + lane;  // this thread's channel
-            const float sw = n_lane < p.N ? p.s_w[n_lane] : 0.0f;
+            const float sw = n_lane < p.N ? p.s_w[FP4 ? 0 : n_lane] : 0.0f;
             if (!mbar_wait(tfull(acc), acc_ph, p.timeout_ns, p.status)) {
                 *abort_flag = 1;
                 break;
@@ -399,7 +461,7 @@ int launch_w8a16_tensor(const __nv_bfloat16* x, const uint8_t* wq, const float* 
     if (rc) return rc;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status))) return rc;
-    Params p{wq, s_w, y, M, N, K, status, watchdog_ns()};
+    Params p{wq, s_w, nullptr, y, M, N, K, status, watchdog_ns()};
     // a wave of 256-token tiles takes about 1.25 times as long as one of
     // 128-token tiles (17.7 against 14.0 us for 6144 x 2048 weights) for
     // twice the work (the same MMA count, the epilogue not overlapped): take
@@ -422,6 +484,50 @@ int launch_w8a16_tensor(const __nv_bfloat16* x, const uint8_t* wq, const float* 
     return cuda_check(launch_pdl(w16_gemm_kernel<128>, dim3(grid), dim3(THREADS), Cfg<128>::SMEM_BYTES, st, 1,
                                  tx, p),
                       "w8a16 tensor-core GEMM launch");
+}
+
+// NVFP4 weight-only GEMM on the tensor cores (arguments validated by the
+// caller): x BF16 [M, K], codes [N, K/2], tiled scales, N % 128 == 0, K % 64 == 0.
+int launch_nvfp4_w4a16_tensor(const __nv_bfloat16* x, const uint8_t* q, const uint8_t* sf, const float* g,
+                              __nv_bfloat16* y, int M, int N, int K, cudaStream_t st) {
+    using namespace w16;
+    DeviceInfo di;
+    int rc = current_device_info(&di);
+    if (rc) return rc;
+    static std::atomic<uint64_t> attr_done[64];
+    rc = once_per_context(attr_done, di.device, [] {
+        auto set = [](const void* f, size_t bytes) {
+            return cuda_check(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)),
+                              "cudaFuncSetAttribute(w16 nvfp4)");
+        };
+        int r = set(reinterpret_cast<const void*>(w16_gemm_kernel<32, true>), Cfg<32>::SMEM_BYTES);
+        if (!r) r = set(reinterpret_cast<const void*>(w16_gemm_kernel<64, true>), Cfg<64>::SMEM_BYTES);
+        if (!r) r = set(reinterpret_cast<const void*>(w16_gemm_kernel<128, true>), Cfg<128>::SMEM_BYTES);
+        if (!r) r = set(reinterpret_cast<const void*>(w16_gemm_kernel<256, true>), Cfg<256>::SMEM_BYTES);
+        return r;
+    });
+    if (rc) return rc;
+    uint32_t* status = nullptr;
+    if ((rc = device_status_word(&status))) return rc;
+    Params p{q, g, sf, y, M, N, K, status, watchdog_ns()};
+    // the tile width as in launch_w8a16_tensor; narrow tiles for few tokens
+    const int64_t nn = (N + TILE_N - 1) / TILE_N;
+    const int64_t t128 = (M + 127) / 128 * nn, t256 = (M + 255) / 256 * nn;
+    const int64_t w128 = (t128 + di.num_sms - 1) / di.num_sms, w256 = (t256 + di.num_sms - 1) / di.num_sms;
+    const int tm = M <= 32 ? 32 : M <= 64 ? 64 : 125 * w256 < 100 * w128 ? 256 : 128;
+    CUtensorMap tx;
+    if ((rc = make_tmap_2d(&tx, x, 2, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K) * 2,
+                           BOXE, tm, true)))
+        return rc;
+    const int64_t tiles = (M + tm - 1) / tm * nn;
+    const dim3 grid(static_cast<unsigned>(tiles < di.num_sms ? tiles : di.num_sms));
+    auto go = [&](auto kernel, size_t bytes) {
+        return cuda_check(launch_pdl(kernel, grid, dim3(THREADS), bytes, st, 1, tx, p), "nvfp4 w4a16 tensor-core GEMM launch");
+    };
+    if (tm == 32) return go(w16_gemm_kernel<32, true>, Cfg<32>::SMEM_BYTES);
+    if (tm == 64) return go(w16_gemm_kernel<64, true>, Cfg<64>::SMEM_BYTES);
+    if (tm == 128) return go(w16_gemm_kernel<128, true>, Cfg<128>::SMEM_BYTES);
+    return go(w16_gemm_kernel<256, true>, Cfg<256>::SMEM_BYTES);
 }
 
 namespace w16 {
