@@ -98,7 +98,7 @@ __host__ __device__ inline Smem smem_layout(int slot_bytes, int P, int pitch, in
     s.unshift = s.x + P * pitch;
     s.items = s.unshift + ((P * 8 + 15) & ~15);
     s.route = s.items + 2 * W * static_cast<int>(sizeof(Item));
-    s.own = s.route + (routed ? 4 * (E + 4 * S + 3) : 16);
+    s.own = s.route + (routed ? 4 * (E + 4 * S + 18) : 16);
     s.own = (s.own + 15) & ~15;
     s.total = s.own + (own ? S * 16 * 4 : 0);
     return s;
@@ -373,16 +373,17 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
         r.jobs = *jobs;
         return r;
     }
-    for (int e = threadIdx.x; e < a.E; e += THREADS) count[e] = 0;
-    int id[MAX_S / THREADS], rank[MAX_S / THREADS];
+    constexpr int SLOTS = MAX_S / THREADS, EXPERTS = MAX_E / THREADS;  // per thread
+    int id[SLOTS], rank[SLOTS];
 #pragma unroll
-    for (int i = 0; i < MAX_S / THREADS; ++i) {
+    for (int i = 0; i < SLOTS; ++i) {
         const int s = threadIdx.x + i * THREADS;
         id[i] = s < a.S ? a.ids[s] : -1;
     }
+    for (int e = threadIdx.x; e < a.E; e += THREADS) count[e] = 0;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MAX_S / THREADS; ++i) {
+    for (int i = 0; i < SLOTS; ++i) {
         rank[i] = 0;
         if (id[i] >= 0 && id[i] < a.E) {
             rank[i] = atomicAdd(&count[id[i]], 1);
@@ -392,53 +393,65 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
         }
     }
     __syncthreads();
-    if (threadIdx.x < 32) {
-        int nj = 0, tot = 0, chosen = 0;
-        for (int e0 = 0; e0 < a.E; e0 += 32) {
-            const int c = e0 + lane < a.E ? count[e0 + lane] : 0;
-            const int own = c | ((c + columns - 1) / columns) << 16;
-            const int incl = scan(own);
-            emit(e0 + lane, c, tot + ((incl - own) & 0xFFFF), nj + ((incl - own) >> 16));
-            if (c > 0) count[e0 + lane] = (tot + ((incl - own) & 0xFFFF)) | c << 16;  // first entry, slots
-            const int all = __shfl_sync(0xffffffffu, incl, 31);
-            nj += all >> 16;
-            chosen += __popc(__ballot_sync(0xffffffffu, c > 0));
-            tot += all & 0xFFFF;
-        }
-        if (lane == 0) {
-            r.start[nj] = tot;
-            jobs[0] = nj;
-            jobs[1] = chosen;
+    // scan over the experts, EXPERTS consecutive ones per thread: slots in the
+    // low half, jobs in the high half
+    const int e0 = threadIdx.x * EXPERTS;
+    int c[EXPERTS], own = 0;
+    bool split = false;  // an expert with several jobs
+#pragma unroll
+    for (int k = 0; k < EXPERTS; ++k) {
+        c[k] = e0 + k < a.E ? count[e0 + k] : 0;
+        own += c[k] | ((c[k] + columns - 1) / columns) << 16;
+        split |= c[k] > columns;
+    }
+    int incl = scan(own);
+    if (lane == 31) jobs[threadIdx.x / 32] = incl;
+    __syncthreads();
+    {
+        const int w = threadIdx.x / 32;
+        incl += __reduce_add_sync(0xffffffffu, lane < w ? jobs[lane] : 0);
+    }
+    int first = (incl - own) & 0xFFFF, at = (incl - own) >> 16;
+#pragma unroll
+    for (int k = 0; k < EXPERTS; ++k) {
+        if (c[k] > 0) {
+            emit(e0 + k, c[k], first, at);
+            count[e0 + k] = first | c[k] << 16;  // first entry, slots
+            first += c[k];
+            at += (c[k] + columns - 1) / columns;
         }
     }
-    __syncthreads();
-    r.jobs = *jobs;
-    // an expert with several jobs: its slots in ascending order
-    if (r.jobs > jobs[1]) {
+    if (threadIdx.x == THREADS - 1) {
+        r.start[incl >> 16] = incl & 0xFFFF;
+        jobs[THREADS / 32] = incl >> 16;
+    }
+    if (__syncthreads_or(split)) {
+        // an expert's slots in ascending order
 #pragma unroll
-    for (int i = 0; i < MAX_S / THREADS; ++i)
-        if (id[i] >= 0) r.row[(count[id[i]] & 0xFFFF) + rank[i]] = threadIdx.x + i * THREADS;
-    __syncthreads();
+        for (int i = 0; i < SLOTS; ++i)
+            if (id[i] >= 0) r.row[(count[id[i]] & 0xFFFF) + rank[i]] = threadIdx.x + i * THREADS;
+        __syncthreads();
 #pragma unroll
-    for (int i = 0; i < MAX_S / THREADS; ++i)
-        if (id[i] >= 0) {
-            const int c = count[id[i]] >> 16, s = threadIdx.x + i * THREADS;
-            const int* list = r.row + (count[id[i]] & 0xFFFF);
-            if (c > columns) {
-                int below = 0;
-                for (int k = 0; k < c; ++k) below += list[k] < s;
-                rank[i] = below;
+        for (int i = 0; i < SLOTS; ++i)
+            if (id[i] >= 0) {
+                const int n = count[id[i]] >> 16, s = threadIdx.x + i * THREADS;
+                const int* list = r.row + (count[id[i]] & 0xFFFF);
+                if (n > columns) {
+                    int below = 0;
+                    for (int k = 0; k < n; ++k) below += list[k] < s;
+                    rank[i] = below;
+                }
             }
-        }
-    __syncthreads();
+        __syncthreads();
     }
 #pragma unroll
-    for (int i = 0; i < MAX_S / THREADS; ++i)
+    for (int i = 0; i < SLOTS; ++i)
         if (id[i] >= 0) {
-            const int s = threadIdx.x + i * THREADS, at = (count[id[i]] & 0xFFFF) + rank[i];
-            r.slots[at] = s;
-            r.row[at] = MODE == UP ? s / a.topk : s;
+            const int s = threadIdx.x + i * THREADS, to = (count[id[i]] & 0xFFFF) + rank[i];
+            r.slots[to] = s;
+            r.row[to] = MODE == UP ? s / a.topk : s;
         }
+    r.jobs = jobs[THREADS / 32];
     __syncthreads();
     return r;
 }
@@ -493,39 +506,27 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     auto job_start = [&](int j) { return MODE == DENSE ? min(j * columns, a.S) : rt.start[j]; };
 
     // The share of this CTA. UP, DOWN, DENSE: tiles of 16 rows, of one job
-    // after another; a segment is a job's part of the share. OWN: rows of the
-    // output, for every job; a segment is up to 16 rows, its tiles the jobs.
+    // after another: tile f of the share is tile (u0 + f) % job_tiles of job
+    // (u0 + f) / job_tiles. OWN: rows of the output, in tiles of 16, each for
+    // every job: tile f is job f % jobs of rows 16 (f / jobs) of the share.
     const int job_tiles = (N + 15) >> 4;
-    int spare, skip = 0, rest;
+    int spare;
     const int each = divide(MODE == OWN ? N : rt.jobs * job_tiles, gridDim.x, a.grid_inv, spare);
     const int u0 = each * static_cast<int>(blockIdx.x) + min(static_cast<int>(blockIdx.x), spare);
     const int share = each + (static_cast<int>(blockIdx.x) < spare ? 1 : 0);
-    const int first = MODE == OWN ? 0 : divide(u0, job_tiles, a.tiles_inv, skip);
-    const int nseg = share == 0 || rt.jobs == 0 ? 0
-                     : MODE == OWN              ? (share + 15) >> 4
-                                                : divide(skip + share - 1, job_tiles, a.tiles_inv, rest) + 1;
-    // places [pb, pe) and tiles of a segment
-    auto segment = [&](int s, int& pb, int& pe) {
-        if constexpr (MODE == OWN) {
-            pb = u0 + 16 * s;
-            pe = min(pb + 16, u0 + share);
-            return rt.jobs;
-        } else {
-            const int t0 = s == 0 ? skip : 0;
-            pb = 16 * t0;
-            pe = N;
-            return min(skip + share - s * job_tiles, job_tiles) - t0;
-        }
-    };
-    // Segments are taken in groups whose operand rows are staged together, as
-    // many as fit; the tiles of a group are shared out to the warps without a
-    // barrier. OWN, by_token: all operand rows are staged at the start.
-    auto group_end = [&](int s0) {
-        int s1 = s0 + 1;
-        if (by_token) return nseg;
-        if constexpr (MODE != OWN)
-            while (s1 < nseg && job_start(first + s1 + 1) - job_start(first + s0) <= a.P) ++s1;
-        return s1;
+    const int total = MODE == OWN ? ((share + 15) >> 4) * rt.jobs : share;
+    auto tile_job = [&](int f, int& tile) { return divide(u0 + f, job_tiles, a.tiles_inv, tile); };
+    // Tiles are taken in groups whose operand rows are staged together: whole
+    // jobs, as many as fit, shared out to the warps without a barrier. by_token:
+    // one group; OWN: a group is 16 rows, the operand is staged for all of them.
+    auto group_end = [&](int f) {
+        if (MODE == OWN) return f + rt.jobs;
+        if (by_token) return share;
+        int tile, j = tile_job(f, tile);
+        const int most = job_start(j) + a.P;
+        ++j;
+        while (j * job_tiles < u0 + share && job_start(j + 1) <= most) ++j;
+        return min(j * job_tiles - u0, share);
     };
 
     // ks warps share a tile's K, so that WARPS / ks teams work on tiles of
@@ -533,9 +534,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     // round's sums counted as one piece (a tile per warp needs none).
     int ks = 1, lt = LOG;  // teams = 1 << lt
     {
-        int best = 0x7fffffff, tiles = 0, pb, pe;
-        for (int s = 0; s < nseg && s < 3; ++s) tiles += segment(s, pb, pe);
-        if (MODE == OWN) tiles = rt.jobs;
+        const int tiles = MODE == OWN ? rt.jobs : share;
+        int best = 0x7fffffff;
 #pragma unroll
         for (int l = 0; l <= LOG; ++l) {
             const int k = WARPS >> l;
@@ -547,30 +547,30 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
 
     // ---- weight stream: this warp's pieces in order, DEPTH of them in flight
     // in lane-private places of the ring (a lane reads back what it copied).
-    // Rows past the segment repeat its first row (their sums are not stored);
-    // bytes past the end of a row are zeros.
+    // Rows past the tile's end repeat its first row (their sums are not
+    // stored); bytes past the end of a row are zeros.
     const int pieces = kslice < kp ? (kp - kslice + ks - 1) >> (LOG - lt) : 0;  // of a tile, for this warp
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * DEPTH * G::SLOT);
-    int rseg = -1, rgroup = 0, rtile = team - teams, rtiles = 0, rpb = 0, rpe = 0, rleft = 0, rrem = 0;
+    int rf = team - teams, rend = 0, rleft = 0, rrem = 0;  // tile to request, end of its group
+    int rrow = u0 - 16;                                    // OWN: first row of the group
     const uint8_t *wp0 = nullptr, *wp1 = nullptr, *sp0 = nullptr, *sp1 = nullptr;
     auto next_tile = [&](uint32_t place) {
-        rtile += teams;
-        while (rtile >= rtiles) {
-            rtile -= rtiles;
-            if (++rseg >= nseg) {
-                rseg = nseg, rtiles = 0x7fffffff;
+        rf += teams;
+        while (rf >= rend) {
+            if (rend >= total) {
+                rf = rend = total;
                 return;
             }
-            if (rseg == rgroup) {
-                rgroup = group_end(rseg);
-                rtile = team;
-            }
-            rtiles = segment(rseg, rpb, rpe);
+            rf = rend + team;
+            rend = group_end(rend);
+            if (MODE == OWN) rrow += 16;
         }
-        const int e = job_expert(MODE == OWN ? rtile : first + rseg);
-        const int p = rpb + (MODE == OWN ? 0 : 16 * rtile) + g;
-        const uint32_t row0 = static_cast<uint32_t>(e * N + place_to_row<FMT>(p < rpe ? p : rpb));
-        const uint32_t row1 = static_cast<uint32_t>(e * N + place_to_row<FMT>(p + 8 < rpe ? p + 8 : rpb));
+        int tile = 0;
+        const int j = MODE == OWN ? rf - rend + rt.jobs : tile_job(rf, tile);
+        const int e = job_expert(j);
+        const int pb = MODE == OWN ? rrow : 16 * tile, p = pb + g, pe = MODE == OWN ? u0 + share : N;
+        const uint32_t row0 = static_cast<uint32_t>(e * N + place_to_row<FMT>(p < pe ? p : pb));
+        const uint32_t row1 = static_cast<uint32_t>(e * N + place_to_row<FMT>(p + 8 < pe ? p + 8 : pb));
         const int at = 64 * kslice + 16 * t;
         wp0 = a.w.q + static_cast<uint64_t>(row0) * static_cast<uint32_t>(row_bytes) + at;
         wp1 = a.w.q + static_cast<uint64_t>(row1) * static_cast<uint32_t>(row_bytes) + at;
@@ -590,7 +590,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         }
     };
     auto request = [&](uint32_t place) {
-        if (rleft == 0 && rseg < nseg) next_tile(place);
+        if (rleft == 0 && rf < total) next_tile(place);
         if (rleft > 0) {
             const bool past = rrem <= 0;
             cp_async16(place + 16 * lane, wp0, past);
@@ -608,16 +608,17 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         }
         cp_async_commit();
     };
-    if (pieces == 0) rseg = nseg;
+    if (pieces == 0) rf = rend = total;
+    // the first group's operand rows, in the order of the slot list
     if constexpr (MODE == UP || MODE == DENSE) {
-        if (!by_token && nseg > 0) {
-            const int base = job_start(first);
-            load_early(job_start(first + group_end(0)) - base,
-                       [&](int i) { return in + static_cast<int64_t>(MODE == DENSE ? base + i : rt.row[base + i]) * K; });
+        if (!by_token && total > 0) {
+            int tile;
+            const int base = job_start(tile_job(0, tile)), n = job_start(tile_job(group_end(0) - 1, tile) + 1) - base;
+            load_early(n, [&](int i) { return in + static_cast<int64_t>(MODE == DENSE ? base + i : rt.row[base + i]) * K; });
         }
     }
     // fill the ring: the first tile's pieces side by side, then the next tiles'
-    if (rseg < nseg) next_tile(ring);
+    if (rf < total) next_tile(ring);
     const int ahead = min(rleft, DEPTH);
 #pragma unroll
     for (int d = 0; d < DEPTH; ++d) {
@@ -651,36 +652,34 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         grid_launch_dependents();
     }
     int buf = 0;
-    for (int s0 = 0; s0 < nseg;) {
-        const int s1 = group_end(s0);
+    for (int f0 = 0, f1; f0 < total; f0 = f1) {
+        f1 = group_end(f0);
         // ---- operand rows, in the order of the slot list (OWN: those of slots
         // without an expert are not in it), or the tokens
-        const int base = MODE == OWN ? 0 : job_start(first + s0);
-        if (!(MODE == OWN || by_token) || s0 == 0) {
-            if (s0 > 0) __syncthreads();
-            const int n = by_token ? a.T : job_start(MODE == OWN ? rt.jobs : first + s1) - base;
+        int base = 0, unused;
+        if (MODE != OWN && !by_token) base = job_start(tile_job(f0, unused));
+        if (!(MODE == OWN || by_token) || f0 == 0) {
+            if (f0 > 0) __syncthreads();
+            const int n = by_token ? a.T : job_start(MODE == OWN ? rt.jobs : tile_job(f1 - 1, unused) + 1) - base;
             stage_rows<FMT, WARPS, In>(n, K, xs, a.pitch, unshift, amax, early, loaded, [&](int i) {
                 return in + static_cast<int64_t>(by_token ? i : MODE == DENSE ? base + i : rt.row[base + i]) * K;
             });
             loaded = false;
         }
-        int tiles = 0, pb = 0, pe = 0;
-        for (int s = s0; s < s1; ++s) tiles += segment(s, pb, pe);
-        int cs = s0, ct = team, ctiles = segment(s0, pb, pe);  // this team's tile
-        for (int tile0 = 0; tile0 < tiles; tile0 += teams, ct += teams) {
-            const bool mine = tile0 + team < tiles;
+        const int own_row = MODE == OWN ? 16 * (f0 / max(rt.jobs, 1)) : 0;  // of the share
+        for (int fr = f0; fr < f1; fr += teams) {
+            const bool mine = fr + team < f1;
             // one group of columns: two chains of MMAs, added at the end
             constexpr int CHAINS = GMAX == 1 ? 2 : 1;
             float acc[GMAX * CHAINS][4];
 #pragma unroll
             for (int q = 0; q < GMAX * CHAINS; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
-            int start = 0, n = 0;
+            int start = 0, n = 0, p0 = u0 + own_row;
+            const int pe = MODE == OWN ? u0 + share : N;
             if (mine) {
-                while (ct >= ctiles) {
-                    ct -= ctiles;
-                    ctiles = segment(++cs, pb, pe);
-                }
-                const int j = MODE == OWN ? ct : first + cs;
+                int tile = 0;
+                const int j = MODE == OWN ? fr + team - f0 : tile_job(fr + team, tile);
+                if (MODE != OWN) p0 = 16 * tile;
                 start = job_start(j);
                 n = job_start(j + 1) - start;
                 // columns past n repeat the first one: their sums are not stored
@@ -770,11 +769,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                     static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(at + c) * N + row] = __float2bfloat16_rn(v);
                 } else {
                     const int sl = rt.slots[at + c];
-                    if constexpr (MODE == OWN) reinterpret_cast<float*>(smem + L.own)[sl * 16 + (p - u0 - 16 * s0)] = v;
+                    if constexpr (MODE == OWN) reinterpret_cast<float*>(smem + L.own)[sl * 16 + (p - u0 - own_row)] = v;
                     else static_cast<float*>(a.out)[static_cast<int64_t>(sl) * N + row] = v;
                 }
             };
-            const int p0 = pb + (MODE == OWN ? 0 : 16 * ct);
             if (ks == 1) {
                 if (mine) {
 #pragma unroll
@@ -814,10 +812,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             // every job has given its part of these 16 rows
             __syncthreads();
             const float* ov = reinterpret_cast<const float*>(smem + L.own);
-            segment(s0, pb, pe);
             for (int i = threadIdx.x; i < a.T * 16; i += THREADS) {
-                const int tk = i >> 4, p = pb + (i & 15);
-                if (p >= pe) continue;
+                const int tk = i >> 4, p = u0 + own_row + (i & 15);
+                if (p >= u0 + share) continue;
                 float y = 0.0f;
                 for (int j = 0; j < a.topk; ++j) {
                     const int sl = tk * a.topk + j;
@@ -828,7 +825,6 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             }
             __syncthreads();
         }
-        s0 = s1;
     }
     if constexpr (MODE == OWN) {
         if (rt.jobs == 0) {  // no token has an expert
