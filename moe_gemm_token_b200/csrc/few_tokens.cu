@@ -31,11 +31,16 @@ enum Mode { UP = 0, DOWN = 1, OWN = 2, DENSE = 3 };
 // Geometry by warps per CTA: 8 warps leave room on an SM for a CTA of the next
 // kernel, whose prologue then overlaps (few weights per SM: latency); 16 take
 // an SM by themselves and share one staged operand (many weights per SM).
-// depth: pieces in flight per warp. 64 KB per SM cover the memory latency.
-template <int W, int GMAX, int MODE>
+// DEPTH: pieces in flight per warp; 64 KB per SM cover the memory latency.
+// 8 warps: OWN shares the SM with the up-projection and reads up to 11 of its
+// pieces ahead while that one runs. 16 warps: what is left beside the operand
+// rows (measured per call: FP8, 32 tokens, 4 -> 6 pieces 63.0 -> 61.8 us;
+// NVFP4 is bound by its widening instructions, 64 tokens 30.7 -> 31.7 us).
+template <int FMT, int MODE, int GMAX, int W>
 struct Cta {
-    // fewer pieces leave room for the operand: 16 rows of K = 4096 (DENSE)
-    static constexpr int DEPTH = W == 8 ? 8 : GMAX == 1 || (GMAX == 2 && MODE != DENSE) ? 4 : 3;
+    static constexpr int DEPTH = W == 8     ? (FMT == NVFP4 ? 8 : MODE == OWN ? 11 : MODE == UP ? 6 : 8)
+                                 : FMT == FP8 ? (GMAX <= 2 ? 6 : 4)
+                                              : (MODE == DENSE && GMAX == 2 ? 3 : 4);
 };
 
 // Per-format geometry. A piece is 16 rows by 64 bytes: lane (g, t) = (lane / 4,
@@ -89,18 +94,18 @@ __device__ __forceinline__ int divide(uint32_t n, uint32_t d, uint32_t inv, int&
 struct Smem {
     int part, x, unshift, items, route, own, total;
 };
-template <int W, int GMAX, int MODE>
+template <int FMT, int MODE, int GMAX, int W>
 __host__ __device__ inline Smem smem_layout(int slot_bytes, int P, int pitch, int E, int S) {
     constexpr bool routed = MODE != DENSE, own = MODE == OWN;
     Smem s;
-    s.part = W * Cta<W, GMAX, MODE>::DEPTH * slot_bytes;
+    s.part = W * Cta<FMT, MODE, GMAX, W>::DEPTH * slot_bytes;
     s.x = s.part + (GMAX == 1 ? 2 : 1) * W * 512 * GMAX;
     s.unshift = s.x + P * pitch;
     s.items = s.unshift + ((P * 8 + 15) & ~15);
     s.route = s.items + 2 * W * static_cast<int>(sizeof(Item));
     s.own = s.route + (routed ? 4 * (E + 4 * S + 18) : 16);
     s.own = (s.own + 15) & ~15;
-    s.total = s.own + (own ? S * 16 * 4 : 0);
+    s.total = s.own + (own ? S * 17 * 4 : 0);
     return s;
 }
 
@@ -459,11 +464,11 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
 template <int FMT, int MODE, int GMAX, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args a) {
     using G = Geo<FMT>;
-    constexpr int THREADS = WARPS * 32, DEPTH = Cta<WARPS, GMAX, MODE>::DEPTH;
+    constexpr int THREADS = WARPS * 32, DEPTH = Cta<FMT, MODE, GMAX, WARPS>::DEPTH;
     constexpr int LOG = WARPS == 8 ? 3 : 4;
     using In = typename std::conditional<MODE == UP || MODE == DENSE, __nv_bfloat16, float>::type;
     extern __shared__ __align__(128) uint8_t smem[];
-    const Smem L = smem_layout<WARPS, GMAX, MODE>(G::SLOT, a.P, a.pitch, a.E, a.S);
+    const Smem L = smem_layout<FMT, MODE, GMAX, WARPS>(G::SLOT, a.P, a.pitch, a.E, a.S);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int g = lane >> 2, t = lane & 3;
     const int N = a.w.N, K = a.w.K;
@@ -647,6 +652,19 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     for (int d = ahead; d < DEPTH; ++d) request(ring + d * G::SLOT);
     uint32_t place = ring;  // of the oldest piece
 
+    // OWN: outputs per slot and row of 16; the slots' routing weights behind them
+    float* own = reinterpret_cast<float*>(smem + L.own);
+    if constexpr (MODE == OWN) {
+        for (int s = threadIdx.x; s < a.S; s += THREADS) {
+            const int id = a.ids[s];
+            own[a.S * 16 + s] = a.tw[s];
+            // outputs of a slot without an expert stay zero, and so does its weight
+            if (id < 0 || id >= a.E) {
+                own[a.S * 16 + s] = 0.0f;
+                for (int i = 0; i < 16; ++i) own[s * 16 + i] = 0.0f;
+            }
+        }
+    }
     if constexpr (MODE == DOWN || MODE == OWN) {
         grid_dependency_wait();
         grid_launch_dependents();
@@ -769,7 +787,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                     static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(at + c) * N + row] = __float2bfloat16_rn(v);
                 } else {
                     const int sl = rt.slots[at + c];
-                    if constexpr (MODE == OWN) reinterpret_cast<float*>(smem + L.own)[sl * 16 + (p - u0 - own_row)] = v;
+                    if constexpr (MODE == OWN) own[sl * 16 + (p - u0 - own_row)] = v;
                     else static_cast<float*>(a.out)[static_cast<int64_t>(sl) * N + row] = v;
                 }
             };
@@ -811,16 +829,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         if constexpr (MODE == OWN) {
             // every job has given its part of these 16 rows
             __syncthreads();
-            const float* ov = reinterpret_cast<const float*>(smem + L.own);
             for (int i = threadIdx.x; i < a.T * 16; i += THREADS) {
                 const int tk = i >> 4, p = u0 + own_row + (i & 15);
                 if (p >= u0 + share) continue;
                 float y = 0.0f;
-                for (int j = 0; j < a.topk; ++j) {
-                    const int sl = tk * a.topk + j;
-                    const int id = a.ids[sl];
-                    if (id >= 0 && id < a.E) y = fmaf(a.tw[sl], ov[sl * 16 + (i & 15)], y);
-                }
+                for (int sl = tk * a.topk; sl < (tk + 1) * a.topk; ++sl) y = fmaf(own[a.S * 16 + sl], own[sl * 16 + (i & 15)], y);
                 static_cast<__nv_bfloat16*>(a.out)[static_cast<int64_t>(tk) * N + place_to_row<FMT>(p)] = __float2bfloat16_rn(y);
             }
             __syncthreads();
@@ -953,14 +966,21 @@ int launch_few(const DeviceInfo& di, Args a, bool latency, cudaStream_t st) {
     using G = Geo<FMT>;
     static std::atomic<uint64_t> done[64];
     int rc = once_per_context(done, di.device, [&] {
-        return cuda_check(cudaFuncSetAttribute(few_kernel<FMT, MODE, GMAX, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               di.max_smem_optin),
-                          "cudaFuncSetAttribute(few tokens)");
+        const auto f = few_kernel<FMT, MODE, GMAX, W>;
+        int r = cuda_check(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, di.max_smem_optin),
+                           "cudaFuncSetAttribute(few tokens)");
+        // the whole carveout: an SM set up for less would not take the next
+        // kernel's CTA beside this one's (FP8, one token: 16.5 -> 15.1 us a call)
+        if (!r)
+            r = cuda_check(cudaFuncSetAttribute(f, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                cudaSharedmemCarveoutMaxShared),
+                           "cudaFuncSetAttribute(few tokens, carveout)");
+        return r;
     });
     if (rc) return rc;
     a.pitch = operand_pitch<FMT>(a.w.K);
     constexpr int HALF = 112 * 1024;  // two CTAs per SM
-    auto bytes = [&](int P) { return smem_layout<W, GMAX, MODE>(G::SLOT, P, a.pitch, a.E, a.S).total; };
+    auto bytes = [&](int P) { return smem_layout<FMT, MODE, GMAX, W>(G::SLOT, P, a.pitch, a.E, a.S).total; };
     const int base = bytes(0) + 32;  // rounding
     const int half = (HALF - base) / (a.pitch + 8), full = (di.max_smem_optin - base) / (a.pitch + 8);
     const int per_job = a.T < 8 * GMAX ? a.T : 8 * GMAX;
