@@ -51,11 +51,11 @@ template <int FMT>
 struct Geo {
     static constexpr int EL = FMT == FP8 ? 64 : 128;     // elements of K per half
     static constexpr int CH = EL / 32;                   // 8-element chunks of K per lane and half
-    // a piece in the ring: codes [half][row of the lane][32][16]; then 4-byte
-    // words per lane: FP8 the channel scales of its two rows, NVFP4 their block
-    // scales for each half, and the global scale
-    static constexpr int WORDS = 2048;
-    static constexpr int SLOT = WORDS + (FMT == FP8 ? 256 : 640);
+    // a piece in the ring: codes [half][row of the lane][32][16]; then words:
+    // FP8 per lane the channel scales of its two rows; NVFP4 the block scales
+    // [64-element chunk][16 rows][4], and per lane the global scale
+    static constexpr int WORDS = 2048, GLOBAL = FMT == FP8 ? WORDS : WORDS + 256;
+    static constexpr int SLOT = FMT == FP8 ? WORDS + 256 : GLOBAL + 128;
 };
 
 struct Args {
@@ -556,14 +556,15 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     const int teams = 1 << lt, team = warp >> (LOG - lt), kslice = warp & (ks - 1);
 
     // ---- weight stream: this warp's pieces in order, DEPTH of them in flight
-    // in lane-private places of the ring (a lane reads back what it copied).
+    // in lane-private places of the ring (a lane reads back what it copied; of
+    // the NVFP4 block scales, what the warp copied).
     // Rows past the tile's end repeat its first row (their sums are not
     // stored); bytes past the end of a row are zeros.
     const int pieces = kslice < kp ? (kp - kslice + ks - 1) >> (LOG - lt) : 0;  // of a tile, for this warp
     const uint32_t ring = smem_u32(smem) + static_cast<uint32_t>(warp * DEPTH * G::SLOT);
-    int rf = team - teams, rend = 0, rleft = 0, rrem = 0;  // tile to request, end of its group
+    int rf = team - teams, rend = 0, rleft = 0, rrem = 0, srem = 0;  // tile to request, end of its group
     int rrow = u0 - 16;                                    // OWN: first row of the group
-    const uint8_t *wp0 = nullptr, *wp1 = nullptr, *sp0 = nullptr, *sp1 = nullptr;
+    const uint8_t *wp0 = nullptr, *wp1 = nullptr, *sp = nullptr;
     auto next_tile = [&](uint32_t place) {
         rf += teams;
         while (rf >= rend) {
@@ -590,13 +591,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             cp_async4(place + G::WORDS + 4 * lane, a.w.s + row0, false);
             cp_async4(place + G::WORDS + 128 + 4 * lane, a.w.s + row1, false);
         } else {
-            auto scales = [&](uint32_t row) {
-                return a.w.sf + static_cast<uint64_t>((row >> 7) * (K / 64) + 4 * kslice + (t >> 1)) * 512 + 16 * (row & 31) +
-                       4 * ((row & 127) >> 5);
-            };
-            sp0 = scales(row0);
-            sp1 = scales(row1);
-            cp_async4(place + G::WORDS + 512 + 4 * lane, a.w.s + e, false);
+            // the places' scale words of a chunk are consecutive. 16 places from a
+            // multiple of 16 on (all but OWN): 16 bytes by lane, four chunks of
+            // K; OWN: word by word, two chunks
+            const int pl = MODE == OWN ? min(pb + (lane & 15), pe - 1) : pb + 4 * (lane & 3);
+            const int chunk = 4 * kslice + (MODE == OWN ? lane >> 4 : lane >> 2);
+            sp = a.w.sf + static_cast<uint64_t>((static_cast<uint32_t>(e * N + pl) >> 7) * (K / 64) + chunk) * 512 + 4 * (pl & 127);
+            srem = K / 64 - chunk;
+            cp_async4(place + G::GLOBAL + 4 * lane, a.w.s + e, false);
         }
     };
     // the piece `off` bytes further on in the rows
@@ -606,9 +608,15 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             const bool past = rrem <= off + 64 * h;
             cp_async16(to + 1024 * h + 16 * lane, wp0 + off + 64 * h, past);
             cp_async16(to + 1024 * h + 512 + 16 * lane, wp1 + off + 64 * h, past);
-            if constexpr (FMT == NVFP4) {
-                cp_async4(to + G::WORDS + 256 * h + 4 * lane, sp0 + 16 * off + 1024 * h, past);
-                cp_async4(to + G::WORDS + 256 * h + 128 + 4 * lane, sp1 + 16 * off + 1024 * h, past);
+        }
+        if constexpr (FMT == NVFP4) {
+            const int chunks = off >> 5;  // 32 code bytes each
+            if constexpr (MODE == OWN) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    cp_async4(to + G::WORDS + 128 * h + 4 * lane, sp + 512 * chunks + 1024 * h, srem <= chunks + 2 * h);
+            } else if (lane < 16) {
+                cp_async16(to + G::WORDS + 16 * lane, sp + 512 * chunks, srem <= chunks);
             }
         }
     };
@@ -619,8 +627,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             wp0 += 128 * ks;
             wp1 += 128 * ks;
             if constexpr (FMT == NVFP4) {
-                sp0 += 2048 * ks;
-                sp1 += 2048 * ks;
+                sp += 2048 * ks;
+                srem -= 4 * ks;
             }
             rrem -= 128 * ks;
             --rleft;
@@ -649,8 +657,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     wp0 += 128 * ks * ahead;
     wp1 += 128 * ks * ahead;
     if constexpr (FMT == NVFP4) {
-        sp0 += 2048 * ks * ahead;
-        sp1 += 2048 * ks * ahead;
+        sp += 2048 * ks * ahead;
+        srem -= 4 * ks * ahead;
     }
     rrem -= 128 * ks * ahead;
     rleft -= ahead;
@@ -718,7 +726,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                 float sr[2] = {0.0f, 0.0f};
                 if (pieces > 0) {
                     cp_async_wait_oldest<DEPTH>();
-                    sr[0] = __uint_as_float(ld_shared4(place + G::WORDS + (FMT == FP8 ? 0 : 512) + 4 * lane));
+                    sr[0] = __uint_as_float(ld_shared4(place + G::GLOBAL + 4 * lane));
                     sr[1] = FMT == FP8 ? __uint_as_float(ld_shared4(place + G::WORDS + 128 + 4 * lane)) : sr[0];
                 }
                 auto run = [&](auto groups) {
@@ -726,15 +734,16 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
 #pragma unroll 1
                     for (int i = 0; i < pieces; ++i) {
                         cp_async_wait_oldest<DEPTH>();
+                        if constexpr (FMT == NVFP4) __syncwarp();  // the scales are other lanes' copies
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const uint4 wa = ld_shared16(place + 1024 * h + 16 * lane);
                             const uint4 wb = ld_shared16(place + 1024 * h + 512 + 16 * lane);
                             uint32_t fa[2] = {0, 0}, fb[2] = {0, 0};
                             if constexpr (FMT == NVFP4) {
-                                const uint32_t words = place + G::WORDS + 256 * h + 4 * lane;
+                                const uint32_t words = place + G::WORDS + 64 * (2 * h + (t >> 1)) + 4 * g;
                                 scale_pairs(ld_shared4(words) >> (16 * (t & 1)), fa[0], fa[1]);
-                                scale_pairs(ld_shared4(words + 128) >> (16 * (t & 1)), fb[0], fb[1]);
+                                scale_pairs(ld_shared4(words + 32) >> (16 * (t & 1)), fb[0], fb[1]);
                             }
                             const uint32_t va[4] = {wa.x, wa.y, wa.z, wa.w}, vb[4] = {wb.x, wb.y, wb.z, wb.w};
                             // a chunk of 8 elements of K per lane at a time: rows g and g + 8 as the A
@@ -770,6 +779,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                         }
 #pragma unroll
                         for (int q = 0; q < NG; ++q) xp[q] += ks * (4 * G::EL);
+                        if constexpr (FMT == NVFP4) __syncwarp();  // all lanes have read them
                         request(place);
                         place = place == ring + (DEPTH - 1) * G::SLOT ? ring : place + G::SLOT;
                     }
