@@ -25,6 +25,18 @@ __device__ __forceinline__ uint32_t scale_code(uint32_t amax_bits) {
     return e < 0 ? 0u : static_cast<uint32_t>(e);
 }
 
+// 32 bytes (a whole sector) by one load or store at a 32-byte aligned address.
+__device__ __forceinline__ void load32(const void* p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.u32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store32(void* p, const uint4& a, const uint4& b) {
+    asm volatile("st.global.v8.u32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+                 "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
 // Half a block, 16 consecutive elements: a lane's share. Two lanes make a
 // block, eight a group of four blocks (128 elements, whose scales are one
 // 32-bit word in both layouts).
@@ -32,30 +44,55 @@ template <typename T>
 struct Half;
 template <>
 struct Half<__nv_bfloat16> {
-    uint4 w[2];
-    __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-        w[0] = __ldg(reinterpret_cast<const uint4*>(p));
-        w[1] = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    uint32_t w[8];
+    __device__ __forceinline__ void load(const __nv_bfloat16* p, bool wide) {
+        if (wide) {
+            load32(p, w);
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4*>(p)), b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+        }
+    }
+    // bits of the largest magnitude, as binary32 (an infinity or a NaN is above all others)
+    __device__ __forceinline__ uint32_t amax() const {
+        uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+        for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+        return max(m & 0xFFFF0000u, m << 16);
     }
     __device__ __forceinline__ void get(float (&v)[16]) const {
-        const uint32_t u[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            v[2 * i] = bf16_lo(u[i]);
-            v[2 * i + 1] = bf16_hi(u[i]);
+            v[2 * i] = bf16_lo(w[i]);
+            v[2 * i + 1] = bf16_hi(w[i]);
         }
     }
 };
 template <>
 struct Half<float> {
-    float4 w[4];
-    __device__ __forceinline__ void load(const float* p) {
+    uint32_t w[2][8];
+    __device__ __forceinline__ void load(const float* p, bool wide) {
+        if (wide) {
+            load32(p, w[0]);
+            load32(p + 8, w[1]);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const float4*>(p) + i);
+            for (int i = 0; i < 4; ++i) {
+                const uint4 a = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                uint32_t* o = &w[i / 2][4 * (i % 2)];
+                o[0] = a.x, o[1] = a.y, o[2] = a.z, o[3] = a.w;
+            }
+        }
+    }
+    __device__ __forceinline__ uint32_t amax() const {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) m = max(m, w[i / 8][i % 8] & 0x7FFFFFFFu);
+        return m;
     }
     __device__ __forceinline__ void get(float (&v)[16]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[4 * i] = w[i].x, v[4 * i + 1] = w[i].y, v[4 * i + 2] = w[i].z, v[4 * i + 3] = w[i].w;
+        for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(w[i / 8][i % 8]);
     }
 };
 
@@ -91,7 +128,11 @@ __device__ __forceinline__ uint4 e2m1x8_to_bf16(uint32_t w, float s) {
 }
 
 constexpr int THREADS = 256;
-constexpr int BATCH = 4;   // halves of a lane in flight: 128 bytes of BF16
+// Halves of a lane in flight (128 bytes of BF16 or FP32 read, of BF16 written),
+// and blocks per SM: all resident at once, each thread looping over its share.
+template <typename T>
+constexpr int batch() { return sizeof(T) == 2 ? 4 : 2; }
+constexpr int BATCH = 4, PER_SM = 4, DEQUANT_PER_SM = 8;
 
 // n / d for d > 0 with inv = floor((2^32 - 1) / d), n < 2^32: at most one short.
 __device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t d, uint32_t inv, uint32_t& rest) {
@@ -110,6 +151,7 @@ struct RowArgs {
     uint32_t R, halves, inv;  // rows, halves per row (K / 16), for divide()
     int64_t total;            // halves of all rows (quant, tiled: with the pad rows)
     int tiled, groups;        // tiled scales; K a multiple of 128
+    int wide;                 // every half (quant: of x, dequant: of y) starts on 32 bytes
 };
 
 // Scale byte offset of half h of row r.
@@ -121,7 +163,8 @@ __device__ __forceinline__ int64_t scale_offset(const RowArgs& a, uint32_t r, ui
 // written per BF16 element; a warp reads 1 KB and writes 256 + 16 bytes of
 // consecutive memory per step, BATCH steps in flight.
 template <typename T>
-__global__ void __launch_bounds__(THREADS) quant_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(THREADS, PER_SM) quant_kernel(const RowArgs a) {
+    constexpr int BATCH = batch<T>();
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * THREADS;
@@ -136,21 +179,17 @@ __global__ void __launch_bounds__(THREADS) quant_kernel(const RowArgs a) {
             const bool in = i < a.total;
             r[b] = divide(static_cast<uint32_t>(in ? i : 0), a.halves, a.inv, h[b]);
             live[b] = in && r[b] < a.R;
-            if (live[b]) x[b].load(static_cast<const T*>(a.x) + r[b] * a.ldx + 16 * h[b]);
+            if (live[b]) x[b].load(static_cast<const T*>(a.x) + r[b] * a.ldx + 16 * h[b], a.wide);
         }
 #pragma unroll
         for (int b = 0; b < BATCH; ++b) {
-            float v[16];
-            uint32_t m = 0;
-            if (live[b]) {
-                x[b].get(v);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) m = max(m, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-            }
+            uint32_t m = live[b] ? x[b].amax() : 0u;
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));  // the block's other half
             uint32_t c = live[b] ? scale_code(m) : 0u;       // the pad rows' scales are 0
             if (live[b]) {
                 const float inv = __uint_as_float((254u - c) << 23);  // 2^(127 - c)
+                float v[16];
+                x[b].get(v);
 #pragma unroll
                 for (int k = 0; k < 16; ++k) v[k] = __fmul_rn(v[k], inv);
                 uint2 o = make_uint2(e2m1x8(v), e2m1x8(v + 8));
@@ -171,7 +210,7 @@ __global__ void __launch_bounds__(THREADS) quant_kernel(const RowArgs a) {
 }
 
 // A lane reads back one half: 8.5 bytes read and 32 written.
-__global__ void __launch_bounds__(THREADS) dequant_kernel(const RowArgs a) {
+__global__ void __launch_bounds__(THREADS, DEQUANT_PER_SM) dequant_kernel(const RowArgs a) {
     grid_dependency_wait();
     grid_launch_dependents();
     const int64_t stride = static_cast<int64_t>(gridDim.x) * THREADS;
@@ -194,8 +233,13 @@ __global__ void __launch_bounds__(THREADS) dequant_kernel(const RowArgs a) {
             if (i < a.total) {
                 const float s = e8m0_value(c[b]);
                 uint4* y = reinterpret_cast<uint4*>(a.y) + 2 * i;
-                y[0] = e2m1x8_to_bf16(q[b].x, s);
-                y[1] = e2m1x8_to_bf16(q[b].y, s);
+                const uint4 lo = e2m1x8_to_bf16(q[b].x, s), hi = e2m1x8_to_bf16(q[b].y, s);
+                if (a.wide) {
+                    store32(y, lo, hi);
+                } else {
+                    y[0] = lo;
+                    y[1] = hi;
+                }
             }
         }
     }
@@ -216,7 +260,8 @@ constexpr int64_t MAX_HALVES = 0xF0000000ll;
 
 // Calls launch(rows' arguments, blocks) for consecutive parts of the rows.
 template <typename F>
-int by_parts(const DeviceInfo& di, RowArgs a, int64_t R, int64_t rows, int64_t K, int64_t x_bytes, F&& launch) {
+int by_parts(const DeviceInfo& di, RowArgs a, int64_t R, int64_t rows, int64_t K, int64_t x_bytes, int batch, int per_sm,
+             F&& launch) {
     a.halves = static_cast<uint32_t>(K / 16);
     a.inv = 0xFFFFFFFFu / a.halves;
     const int64_t part = MAX_HALVES / a.halves / 128 * 128;
@@ -229,10 +274,10 @@ int by_parts(const DeviceInfo& di, RowArgs a, int64_t R, int64_t rows, int64_t K
         b.q += r0 * (K / 2);
         b.sf += r0 * (K / 32);
         if (b.y) b.y += r0 * K;
-        // at most 8 blocks of 256 threads per SM, each thread with BATCH halves in flight
-        int64_t blocks = (b.total + THREADS * BATCH - 1) / (THREADS * BATCH);
+        // as many blocks as are resident; fewer halves per thread while SMs would stay without
+        int64_t blocks = (b.total + THREADS * batch - 1) / (THREADS * batch);
         if (blocks < di.num_sms) blocks = (b.total + THREADS - 1) / THREADS;
-        if (blocks > 8ll * di.num_sms) blocks = 8ll * di.num_sms;
+        if (blocks > static_cast<int64_t>(per_sm) * di.num_sms) blocks = static_cast<int64_t>(per_sm) * di.num_sms;
         if (int rc = launch(b, static_cast<unsigned>(blocks))) return rc;
     }
     return METIS_OK;
@@ -270,7 +315,8 @@ extern "C" int metis_quant_mxfp4(const void* x, int x_kind, int64_t R, int64_t K
     a.tiled = tiled;
     a.groups = K % 128 == 0 && aligned(sf, 4);
     const bool bf16 = x_kind == METIS_A_BF16;
-    return by_parts(di, a, R, rows, K, bf16 ? 2 : 4, [&](const RowArgs& b, unsigned blocks) {
+    a.wide = aligned(x, 32) && ldx * (bf16 ? 2 : 4) % 32 == 0;
+    return by_parts(di, a, R, rows, K, bf16 ? 2 : 4, bf16 ? batch<__nv_bfloat16>() : batch<float>(), PER_SM, [&](const RowArgs& b, unsigned blocks) {
         return cuda_check(launch_pdl(bf16 ? quant_kernel<__nv_bfloat16> : quant_kernel<float>, dim3(blocks), dim3(THREADS),
                                      0, static_cast<cudaStream_t>(stream), 1, b),
                           "quant_mxfp4 launch");
@@ -293,8 +339,9 @@ extern "C" int metis_dequant_mxfp4(const uint8_t* q, const uint8_t* sf, int sf_l
     a.q = const_cast<uint8_t*>(q);
     a.sf = const_cast<uint8_t*>(sf);
     a.y = static_cast<__nv_bfloat16*>(y_bf16);
+    a.wide = aligned(y_bf16, 32);
     a.tiled = tiled;
-    return by_parts(di, a, R, R, K, 0, [&](const RowArgs& b, unsigned blocks) {
+    return by_parts(di, a, R, R, K, 0, BATCH, DEQUANT_PER_SM, [&](const RowArgs& b, unsigned blocks) {
         return cuda_check(launch_pdl(dequant_kernel, dim3(blocks), dim3(THREADS), 0, static_cast<cudaStream_t>(stream), 1, b),
                           "dequant_mxfp4 launch");
     });
