@@ -133,35 +133,28 @@ def _check(name, rc):
     return rc
 
 
-def _pointers(name, *tensors):
+def _pointers(name, device, tensors):
     """Device addresses, after the checks that the C entry point cannot make:
-    CUDA tensors of one device, the current one, with dense rows."""
-    device = torch.cuda.current_device()
-    found = []
-    for t in tensors:
-        if t.get_device() != device or not t.is_contiguous():
-            _need(name, t.get_device() == device,
-                  f"tensors must be on the current CUDA device ({device}), got {t.device}")
-            _need(name, False, "tensors must be contiguous")
-        found.append(t.data_ptr())
+    CUDA tensors of the current device with dense rows."""
+    found = [t.data_ptr() for t in tensors if t.get_device() == device and t.is_contiguous()]
+    if len(found) != len(tensors):
+        for t in tensors:
+            if t.get_device() != device:
+                _refuse(name, f"tensors must be on the current CUDA device ({device}), got {t.device}")
+        _refuse(name, "tensors must be contiguous")
     return found
 
 
-def _need(name, ok, what):
-    if not ok:
-        raise ValueError(f"{name}: {what}")
+def _refuse(name, what):
+    raise ValueError(f"{name}: {what}")
 
 
-def _stream(stream):
-    """The stream's handle; None: torch's current stream of the current device,
-    without making a Stream object of it."""
+def _stream(device, stream):
+    """The stream's handle; None: torch's current stream of the device, without
+    making a Stream object of it."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
-
-
-def _bytes(workspace):
-    return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
 
 def _rows(t):
@@ -339,19 +332,21 @@ def metis_moe_nvfp4_workspace_offset(region, T, topk, E, H, I):
 def _moe_few(name, x, topk_ids, topk_w, up, down, packed, y, workspace, act, stream):
     """The two few-token routed layers: shape checks and the call; `up` and
     `down` are (weights, scales...) as the C entry point takes them."""
-    T, H = x.shape
+    shape, slots = x.shape, topk_ids.shape
+    T, H = shape
     E, I, hb = up[0].shape
-    slots = topk_ids.shape
-    _need(name, x.dtype == torch.bfloat16 == y.dtype, "x and y must be torch.bfloat16")
-    _need(name, topk_ids.dtype == torch.int32 and topk_w.dtype == torch.float32,
-          "topk_ids must be torch.int32 and topk_w torch.float32")
-    _need(name, len(slots) == 2 and slots[0] == T and topk_w.shape == slots and y.shape == x.shape,
-          "topk_ids, topk_w and y must match x")
-    _need(name, hb * packed == H and down[0].shape == (E, H, I // packed),
-          "w_up must be [E, I, H] and w_down [E, H, I]")
-    px, pi, pw, py, ws, *weights = _pointers(name, x, topk_ids, topk_w, y, workspace, *up, *down)
-    return _check(name, getattr(load(), name)(
-        px, pi, pw, T, slots[1], E, H, I, *weights, int(act), py, ws, _bytes(workspace), _stream(stream)))
+    if not (x.dtype is torch.bfloat16 and y.dtype is torch.bfloat16):
+        _refuse(name, "x and y must be torch.bfloat16")
+    if not (topk_ids.dtype is torch.int32 and topk_w.dtype is torch.float32):
+        _refuse(name, "topk_ids must be torch.int32 and topk_w torch.float32")
+    if not (len(slots) == 2 and slots[0] == T and topk_w.shape == slots and y.shape == shape):
+        _refuse(name, "topk_ids, topk_w and y must match x")
+    if not (hb * packed == H and down[0].shape == (E, H, I // packed)):
+        _refuse(name, "w_up must be [E, I, H] and w_down [E, H, I]")
+    device = torch.cuda.current_device()
+    px, pi, pw, py, ws, *weights = _pointers(name, device, (x, topk_ids, topk_w, y, workspace, *up, *down))
+    return _check(name, getattr(_lib or load(), name)(
+        px, pi, pw, T, slots[1], E, H, I, *weights, act, py, ws, workspace.nbytes, _stream(device, stream)))
 
 
 def metis_moe_w8a16(x, topk_ids, topk_w, w_up, s_up, w_down, s_down, y, workspace, act=METIS_ACT_NONE,
@@ -359,8 +354,9 @@ def metis_moe_w8a16(x, topk_ids, topk_w, w_up, s_up, w_down, s_down, y, workspac
     """Routed-expert layer in the default maths (FP8 weights, BF16 activations)
     for few tokens; see the C header for shapes."""
     name = "metis_moe_w8a16"
-    _need(name, s_up.shape == w_up.shape[:2] and s_down.shape == w_down.shape[:2] and
-          s_up.dtype == s_down.dtype == torch.float32, "s_up must be FP32 [E, I] and s_down FP32 [E, H]")
+    if not (s_up.shape == w_up.shape[:2] and s_down.shape == w_down.shape[:2] and
+            s_up.dtype is torch.float32 and s_down.dtype is torch.float32 and w_up.element_size() == 1):
+        _refuse(name, "weights must be E4M3 bytes, s_up FP32 [E, I] and s_down FP32 [E, H]")
     return _moe_few(name, x, topk_ids, topk_w, (w_up, s_up), (w_down, s_down), 1, y, workspace, act, stream)
 
 
@@ -369,11 +365,11 @@ def metis_moe_nvfp4_w4a16(x, topk_ids, topk_w, w_up, sf_up, g_up, w_down, sf_dow
     """Routed-expert layer in the default maths with NVFP4 experts, for few
     tokens; weights and tiled scales as in :func:`metis_moe_nvfp4_grouped_gemm`."""
     name = "metis_moe_nvfp4_w4a16"
+    if not (sf_up.nbytes * 8 == w_up.nbytes and sf_down.nbytes * 8 == w_down.nbytes and w_up.element_size() == 1):
+        _refuse(name, "weights must be packed bytes, sf_up and sf_down one byte per 16 elements")
     E = w_up.shape[0]
-    _need(name, sf_up.numel() * 8 == w_up.numel() and sf_down.numel() * 8 == w_down.numel(),
-          "sf_up and sf_down must hold one byte per 16 elements")
-    _need(name, g_up.numel() == E == g_down.numel() and g_up.dtype == g_down.dtype == torch.float32,
-          "g_up and g_down must be FP32 [E]")
+    if not (g_up.numel() == E == g_down.numel() and g_up.dtype is torch.float32 and g_down.dtype is torch.float32):
+        _refuse(name, "g_up and g_down must be FP32 [E]")
     return _moe_few(name, x, topk_ids, topk_w, (w_up, sf_up, g_up), (w_down, sf_down, g_down), 2, y, workspace,
                     act, stream)
 
@@ -384,14 +380,17 @@ def metis_nvfp4_w4a16_gemm(x, qb, sfb, gb, y, workspace=None, stream=None):
     name = "metis_nvfp4_w4a16_gemm"
     M, K = x.shape
     N = qb.shape[0]
-    _need(name, x.dtype == torch.bfloat16 == y.dtype, "x and y must be torch.bfloat16")
-    _need(name, qb.shape == (N, K // 2) and y.shape == (M, N) and sfb.numel() * 16 >= (N + 127) // 128 * 128 * K,
-          "qb must be [N, K/2], sfb its tiled scales and y [M, N]")
-    _need(name, gb.numel() == 1 and gb.dtype == torch.float32, "gb must be one FP32 value")
-    px, pq, ps, pg, py = _pointers(name, x, qb, sfb, gb, y)
-    ws = None if workspace is None else _pointers(name, workspace)[0]
-    return _check(name, load().metis_nvfp4_w4a16_gemm(
-        px, pq, ps, pg, py, M, N, K, ws, _bytes(workspace), _stream(stream)))
+    if not (x.dtype is torch.bfloat16 and y.dtype is torch.bfloat16):
+        _refuse(name, "x and y must be torch.bfloat16")
+    if not (qb.shape == (N, K // 2) and y.shape == (M, N) and sfb.nbytes * 16 >= (N + 127) // 128 * 128 * K):
+        _refuse(name, "qb must be [N, K/2], sfb its tiled scales and y [M, N]")
+    if not (gb.numel() == 1 and gb.dtype is torch.float32):
+        _refuse(name, "gb must be one FP32 value")
+    device = torch.cuda.current_device()
+    px, pq, ps, pg, py = _pointers(name, device, (x, qb, sfb, gb, y))
+    ws, size = (None, 0) if workspace is None else (_pointers(name, device, (workspace,))[0], workspace.nbytes)
+    return _check(name, (_lib or load()).metis_nvfp4_w4a16_gemm(
+        px, pq, ps, pg, py, M, N, K, ws, size, _stream(device, stream)))
 
 
 # ------------------------------------------------------------------ MXFP4
@@ -402,16 +401,21 @@ def metis_quant_mxfp4(x, q, sf, tiled=False, stream=None):
     name = "metis_quant_mxfp4"
     R, K = x.shape
     ldx, step = x.stride()
-    _need(name, x.dtype in (torch.bfloat16, torch.float32), "x must be torch.bfloat16 or torch.float32")
-    _need(name, step == 1 or K == 1, "the rows of x must be contiguous")
+    kind = METIS_A_BF16 if x.dtype is torch.bfloat16 else METIS_A_F32
+    if not (kind == METIS_A_BF16 or x.dtype is torch.float32):
+        _refuse(name, "x must be torch.bfloat16 or torch.float32")
+    if step != 1 and K > 1:
+        _refuse(name, "the rows of x must be contiguous")
     rows = (R + 127) // 128 * 128 if tiled else R
-    _need(name, q.numel() * 2 >= R * K and sf.numel() * 32 >= rows * K, "q or sf is too small")
-    pq, ps = _pointers(name, q, sf)
-    _need(name, x.get_device() == q.get_device(), "x must be on the current CUDA device")
-    kind = METIS_A_F32 if x.dtype == torch.float32 else METIS_A_BF16
-    return _check(name, load().metis_quant_mxfp4(
+    if q.nbytes * 2 < R * K or sf.nbytes * 32 < rows * K:
+        _refuse(name, "q or sf is too small")
+    device = torch.cuda.current_device()
+    pq, ps = _pointers(name, device, (q, sf))
+    if x.get_device() != device:
+        _refuse(name, f"x must be on the current CUDA device ({device}), got {x.device}")
+    return _check(name, (_lib or load()).metis_quant_mxfp4(
         x.data_ptr(), kind, R, K, ldx if R > 1 else K, pq, ps, METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR,
-        _stream(stream)))
+        _stream(device, stream)))
 
 
 def metis_dequant_mxfp4(q, sf, y, tiled=False, stream=None):
@@ -419,11 +423,14 @@ def metis_dequant_mxfp4(q, sf, y, tiled=False, stream=None):
     name = "metis_dequant_mxfp4"
     R, K = y.shape
     rows = (R + 127) // 128 * 128 if tiled else R
-    _need(name, y.dtype == torch.bfloat16, "y must be torch.bfloat16")
-    _need(name, q.numel() * 2 >= R * K and sf.numel() * 32 >= rows * K, "q or sf is too small")
-    pq, ps, py = _pointers(name, q, sf, y)
-    return _check(name, load().metis_dequant_mxfp4(
-        pq, ps, METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR, R, K, py, _stream(stream)))
+    if y.dtype is not torch.bfloat16:
+        _refuse(name, "y must be torch.bfloat16")
+    if q.nbytes * 2 < R * K or sf.nbytes * 32 < rows * K:
+        _refuse(name, "q or sf is too small")
+    device = torch.cuda.current_device()
+    pq, ps, py = _pointers(name, device, (q, sf, y))
+    return _check(name, (_lib or load()).metis_dequant_mxfp4(
+        pq, ps, METIS_SF_TILED if tiled else METIS_SF_ROWMAJOR, R, K, py, _stream(device, stream)))
 
 
 def metis_mxfp4_gemm(qa, sfa, qb, sfb, y, stream=None):
@@ -431,15 +438,17 @@ def metis_mxfp4_gemm(qa, sfa, qb, sfb, y, stream=None):
     holds ceil(M/128)*128 rows."""
     name = "metis_mxfp4_gemm"
     M, N = y.shape
-    K = qb.shape[1] * 2
+    n, kb = qb.shape
     rows = (M + 127) // 128 * 128
-    _need(name, y.dtype == torch.bfloat16, "y must be torch.bfloat16")
-    _need(name, qb.shape[0] == N and qa.shape[1] * 2 == K and qa.shape[0] >= rows,
-          "qa must be [ceil(M/128) * 128, K/2] and qb [N, K/2]")
-    _need(name, sfa.numel() * 32 >= rows * K and sfb.numel() * 32 >= (N + 127) // 128 * 128 * K,
-          "sfa or sfb is too small")
-    pa, psa, pb, psb, py = _pointers(name, qa, sfa, qb, sfb, y)
-    return _check(name, load().metis_mxfp4_gemm(pa, psa, pb, psb, py, M, N, K, _stream(stream)))
+    if y.dtype is not torch.bfloat16:
+        _refuse(name, "y must be torch.bfloat16")
+    if not (n == N and qa.shape[1] == kb and qa.shape[0] >= rows):
+        _refuse(name, "qa must be [ceil(M/128) * 128, K/2] and qb [N, K/2]")
+    if sfa.nbytes * 16 < rows * kb or sfb.nbytes * 16 < (N + 127) // 128 * 128 * kb:
+        _refuse(name, "sfa or sfb is too small")
+    device = torch.cuda.current_device()
+    pa, psa, pb, psb, py = _pointers(name, device, (qa, sfa, qb, sfb, y))
+    return _check(name, (_lib or load()).metis_mxfp4_gemm(pa, psa, pb, psb, py, M, N, 2 * kb, _stream(device, stream)))
 
 
 # ------------------------------------------------------------ shared expert
