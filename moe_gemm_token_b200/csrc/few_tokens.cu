@@ -2,7 +2,34 @@
 // layer with FP8 or NVFP4 experts, and the NVFP4 weight-only product.
 //   h[s] = W_up[e] x[t],  o[s] = W_down[e] h[s],  y[t] = bf16( sum_j w[t, j] o[t, j] )
 // for the slots s = (t, j) with expert e = topk_ids[t, j]; FP32 sums, h and o
-// kept in FP32.
+// kept in FP32. ("Lernex/Metis-1.6-Logos-FP8" and "-Praxis-NVFP4", "What
+// --fast-math does": decoding for a few conversations widens the weights to 16
+// bits as it multiplies, so that the weights are the only thing rounded.)
+//
+// The floor is the chosen experts' weights over HBM; what the kernels lose
+// against it is the latency of the two dependent projections.
+//
+//  * few_kernel, one launch per projection. Each CTA builds the routing from
+//    the ids itself: jobs (an expert with up to 8 or 16 of its slots), whose
+//    16-row tiles are shared out evenly over the CTAs. A warp streams its
+//    tiles' weights through lane-private places of shared memory (cp.async,
+//    64 KB and more in flight per SM, any row granularity: per-row bulk copies
+//    were bound by their issue, 46 per microsecond and CTA), widens them to
+//    FP16 (E4M3, and E2M1 times an E4M3 block scale, are exact FP16 values)
+//    and multiplies with mma.sync m16n8k16, the weights as the 16 rows and the
+//    job's tokens as the 8 columns. A tile's K is split over ks warps when
+//    there are fewer tiles than warps; their sums meet in shared memory.
+//  * The operand (x, then h) is staged as FP16 after a power-of-two shift of
+//    its row: BF16 values keep all their bits within 2^-29 of the row's
+//    largest, FP32 values are rounded to 11 bits (a quarter of what rounding
+//    h to BF16 would cost in the result; the sums stay FP32).
+//  * Few slots (h of all of them fits a CTA): the down-projection's CTAs own
+//    output rows for every job and finish y themselves, two launches in all
+//    (OWN). More: o goes through the workspace and combine_kernel (DOWN).
+//  * The next kernel's prologue (routing, first weights) overlaps this one
+//    through programmatic dependent launch, where an SM has room for both.
+//
+// Sums are added in a fixed order and no result depends on an atomic's order.
 #include <type_traits>
 
 #include "common.cuh"
@@ -31,11 +58,10 @@ enum Mode { UP = 0, DOWN = 1, OWN = 2, DENSE = 3 };
 // Geometry by warps per CTA: 8 warps leave room on an SM for a CTA of the next
 // kernel, whose prologue then overlaps (few weights per SM: latency); 16 take
 // an SM by themselves and share one staged operand (many weights per SM).
-// DEPTH: pieces in flight per warp; 64 KB per SM cover the memory latency.
-// 8 warps: OWN shares the SM with the up-projection and reads up to 11 of its
-// pieces ahead while that one runs. 16 warps: what is left beside the operand
-// rows (measured per call: FP8, 32 tokens, 4 -> 6 pieces 63.0 -> 61.8 us;
-// NVFP4 is bound by its widening instructions, 64 tokens 30.7 -> 31.7 us).
+// DEPTH: pieces (2 KB) in flight per warp. 8 warps: OWN shares the SM with the
+// up-projection and reads 5 of its pieces ahead while that one runs. 16 warps,
+// us per call: FP8, 32 tokens 2 pieces 57.0, 3 pieces 56.4; NVFP4, which its
+// widening instructions bound, 64 tokens 2 pieces 28.3, 3 pieces 29.2.
 template <int FMT, int MODE, int GMAX, int W>
 struct Cta {
     static constexpr int DEPTH = W == 8     ? (FMT == NVFP4 ? 4 : MODE == OWN ? 5 : MODE == UP ? 3 : 4)
@@ -978,11 +1004,12 @@ int check_moe(const char* name, int act, int64_t T, int64_t topk, int64_t E, int
     return METIS_OK;
 }
 
-// Launches few_kernel with as many staged operand rows as are of use (OWN: all
-// slots; else the columns of two jobs) and fit. CTAs of 8 warps go two per SM
-// (for `latency` one, which leaves the other place to the next kernel).
+// Launches few_kernel, one CTA per SM, with as many staged operand rows as are
+// of use (OWN: all slots; else the columns of two jobs) and fit: for 8 warps in
+// half of the shared memory if that holds a job's rows, so that the next
+// kernel's CTAs find room, else in all of it.
 template <int FMT, int MODE, int GMAX, int W>
-int launch_few(const DeviceInfo& di, Args a, bool latency, cudaStream_t st) {
+int launch_few(const DeviceInfo& di, Args a, cudaStream_t st) {
     using G = Geo<FMT>;
     static std::atomic<uint64_t> done[64];
     int rc = once_per_context(done, di.device, [&] {
@@ -999,40 +1026,33 @@ int launch_few(const DeviceInfo& di, Args a, bool latency, cudaStream_t st) {
     });
     if (rc) return rc;
     a.pitch = operand_pitch<FMT>(a.w.K);
-    constexpr int HALF = 112 * 1024;  // two CTAs per SM
     auto bytes = [&](int P) { return smem_layout<FMT, MODE, GMAX, W>(G::SLOT, P, a.pitch, a.E, a.S).total; };
     const int base = bytes(0) + 32;  // rounding
-    const int half = (HALF - base) / (a.pitch + 8), full = (di.max_smem_optin - base) / (a.pitch + 8);
+    const int half = (112 * 1024 - base) / (a.pitch + 8), full = (di.max_smem_optin - base) / (a.pitch + 8);
     const int per_job = a.T < 8 * GMAX ? a.T : 8 * GMAX;
     const int want = MODE == OWN || a.S < 2 * per_job ? a.S : 2 * per_job;
-    int per_sm = 1;
-    a.P = want < full ? want : full;
-    if (W == 8) {
-        const int least = MODE == OWN || want < 8 ? want : 8;
-        if (half >= least) {
-            per_sm = latency ? 1 : 2;
-            a.P = want < half ? want : half;
-        }
-    }
+    const int room = W == 8 && half >= (MODE == OWN ? want : per_job) ? half : full;
+    a.P = want < room ? want : room;
     if (a.P < 1 || (MODE == OWN && a.P < want))
         return fail(METIS_ERR_UNSUPPORTED, "few-token kernel: K=%d is too long", a.w.K);
     // a few tokens that all threads read with one round trip
     a.by_token = MODE == UP && a.T <= a.P && a.T <= W && static_cast<int64_t>(a.T) * a.w.K <= 8 * STAGE_U * 32 * W;
-    a.grid_inv = 0xFFFFFFFFu / static_cast<uint32_t>(di.num_sms * per_sm);
+    a.grid_inv = 0xFFFFFFFFu / static_cast<uint32_t>(di.num_sms);
     a.tiles_inv = 0xFFFFFFFFu / static_cast<uint32_t>((a.w.N + 15) / 16);
-    return cuda_check(launch_pdl(few_kernel<FMT, MODE, GMAX, W>, dim3(di.num_sms * per_sm), dim3(W * 32), bytes(a.P), st, 1, a),
+    return cuda_check(launch_pdl(few_kernel<FMT, MODE, GMAX, W>, dim3(di.num_sms), dim3(W * 32), bytes(a.P), st, 1, a),
                       "few-token kernel launch");
 }
 
 // By the columns that one pass multiplies (8 or 16), the weight bytes that
-// an SM reads, and what fits beside long rows.
+// an SM reads (8 against 16 warps, us per call: FP8, 113 KB a projection and SM
+// 17.1, 17.7; NVFP4, 225 KB 42.5, 32.9), and what fits beside long rows.
 template <int FMT, int MODE>
 int launch_few_by_size(const DeviceInfo& di, const Args& a, int columns, int64_t weight_bytes, cudaStream_t st) {
     const bool small = weight_bytes < di.num_sms * 160ll * 1024;
     const bool long_rows = operand_pitch<FMT>(a.w.K) * 8 > 112 * 1024;
-    if ((columns <= 8 && small) || long_rows) return launch_few<FMT, MODE, 1, 8>(di, a, true, st);
-    if (columns <= 8) return launch_few<FMT, MODE, 1, 16>(di, a, false, st);
-    return launch_few<FMT, MODE, 2, 16>(di, a, false, st);
+    if ((columns <= 8 && small) || long_rows) return launch_few<FMT, MODE, 1, 8>(di, a, st);
+    if (columns <= 8) return launch_few<FMT, MODE, 1, 16>(di, a, st);
+    return launch_few<FMT, MODE, 2, 16>(di, a, st);
 }
 
 template <int FMT>
@@ -1061,10 +1081,10 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
     if ((rc = launch_few_by_size<FMT, UP>(di, a, columns, weight_bytes, st))) return rc;
     a.in = h;
     a.w = down;
-    // few slots: every CTA stages all of h and owns rows of the output
+    // few slots: every CTA stages all of h (beside the ring) and owns rows of the output
     if (S <= 64 && S * operand_pitch<FMT>(down.K) <= 40 * 1024) {
         a.out = y;
-        return launch_few<FMT, OWN, 1, 8>(di, a, true, st);
+        return launch_few<FMT, OWN, 1, 8>(di, a, st);
     }
     a.out = o;
     if ((rc = launch_few_by_size<FMT, DOWN>(di, a, columns, weight_bytes, st))) return rc;
