@@ -262,7 +262,8 @@ METIS_API int metis_moe_fp8_grouped_gemm_noalloc(const void* x_bf16, const int32
  *   holds an infinity or a NaN gets a non-finite output; others are unaffected.
  *   Requires H and I multiples of 16 in [16, 8192], 1 <= topk <= E <= 1024,
  *   0 <= T <= 128 and T * topk <= 1024 (METIS_ERR_UNSUPPORTED beyond: the
- *   grouped GEMM layer is made for more); x, weights and y 16-byte aligned.
+ *   grouped GEMM layer is made for more); x, weights and y 16-byte aligned;
+ *   y overlaps no other argument.
  *   Needs `workspace` of metis_workspace_size(METIS_OP_MOE_W8A16, T, I, H,
  *   topk, E) bytes (256-byte aligned), overwritten: calls that may overlap on
  *   the GPU need one each. */

@@ -25,7 +25,8 @@
  * Conventions are those of metis_fp8.h: device pointers owned by the caller,
  * nothing allocated or synchronised, asynchronous on `stream`, METIS_OK or a
  * negative metis_status with argument errors found before any launch,
- * bounded device waits, bitwise reproducible results.
+ * bounded device waits, bitwise reproducible results. Outputs overlap no
+ * other argument.
  */
 #ifndef METIS_MXFP4_H
 #define METIS_MXFP4_H

@@ -161,7 +161,8 @@ METIS_API int64_t metis_moe_nvfp4_workspace_offset(int region, int64_t T, int64_
  *   Arrays as in metis_moe_nvfp4_grouped_gemm (tiled scales), so that one set
  *   of weights serves both layers; y is required.
  *   Requires H and I multiples of 128 in [128, 8192], 1 <= topk <= E <= 1024,
- *   0 <= T <= 128, T * topk <= 1024; x, codes, tiled scales and y 16-byte aligned.
+ *   0 <= T <= 128, T * topk <= 1024; x, codes, tiled scales and y 16-byte
+ *   aligned; y overlaps no other argument.
  *   workspace  metis_workspace_size(METIS_OP_MOE_NVFP4_W4A16, T, I, H, topk, E)
  *              bytes, 256-byte aligned.
  */
@@ -178,9 +179,14 @@ METIS_API int metis_moe_nvfp4_w4a16(const void* x_bf16, const int32_t* topk_ids,
  * x BF16, the weights widened exactly to 16 bits, FP32 sums.
  *   x [M, K] BF16 (dense rows); qb, sfb, gb as in metis_nvfp4_gemm.
  * K a multiple of 64 in [64, 65536], N a multiple of 128 up to 2^20, M >= 0;
- * x, codes, tiled scales and y 16-byte aligned.
+ * x, codes, tiled scales and y 16-byte aligned; y overlaps no other argument.
+ * Up to 16 tokens the weights are streamed past them as in the layer above (x
+ * keeps its BF16 values, elements below 2^-29 of a token's largest magnitude
+ * lose bits); beyond, they are multiplied as BF16.
  *   workspace  metis_workspace_size(METIS_OP_NVFP4_W4A16, M, N, K, 0, 0)
- *              bytes, 256-byte aligned; 0 (NULL allowed) for few tokens.
+ *              bytes, 256-byte aligned: 0 (NULL allowed) up to 2048 tokens;
+ *              beyond, the widened weights. Overwritten: calls that may
+ *              overlap on the GPU need one each.
  */
 METIS_API int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, const uint8_t* sfb,
                                      const float* gb, void* y_bf16, int64_t M, int64_t N, int64_t K,

@@ -13,6 +13,11 @@ only the device status word.
     python -m moe_gemm_token_b200.drive gemm4 M N K [--calls N]
     python -m moe_gemm_token_b200.drive shared [--calls N]
     python -m moe_gemm_token_b200.drive bf16 M N K [--calls N]
+    python -m moe_gemm_token_b200.drive moefew T  [--calls N]
+    python -m moe_gemm_token_b200.drive moe4few T [--calls N]
+    python -m moe_gemm_token_b200.drive w4a16 M N K [--calls N]
+    python -m moe_gemm_token_b200.drive quantmx M K [--calls N]
+    python -m moe_gemm_token_b200.drive gemmmx M N K [--calls N]
 
 Each call is enqueued on the current stream; the script synchronises once at
 the end and exits non-zero if the device status word reports an error.
@@ -39,7 +44,7 @@ def _sf(n, g):
 def main(argv=None):
     ap = argparse.ArgumentParser()
     ap.add_argument("op", choices=["moe", "gemm", "fused", "decode", "w16", "w16w", "quant", "moe4", "gemm4", "shared",
-                                   "bf16"])
+                                   "bf16", "moefew", "moe4few", "w4a16", "quantmx", "gemmmx"])
     ap.add_argument("dims", nargs="*", type=int)
     ap.add_argument("--calls", type=int, default=3)
     a = ap.parse_args(argv)
@@ -96,6 +101,59 @@ def main(argv=None):
         ws = torch.empty(metis.metis_workspace_size(metis.METIS_OP_MOE_NVFP4, T, I, H, k, E),
                          dtype=torch.uint8, device=dev)
         call = lambda: metis.metis_moe_nvfp4_grouped_gemm(x, ids, w, wu, sfu, gu, wd, sfd, gd, y, ws)
+    elif a.op in ("moefew", "moe4few"):
+        # the layers' few-token form: T tokens choosing evenly among the experts
+        (T,) = a.dims
+        H, I, E, k = 2048, 1024, 64, 8
+        x = torch.randn(T, H, device=dev, generator=g).to(torch.bfloat16)
+        top = torch.topk(torch.randn(T, E, device=dev, generator=g), k, dim=1)
+        ids = top.indices.to(torch.int32).contiguous()
+        w = torch.softmax(top.values, dim=1).float().contiguous()
+        y = torch.empty(T, H, dtype=torch.bfloat16, device=dev)
+        op = metis.METIS_OP_MOE_W8A16 if a.op == "moefew" else metis.METIS_OP_MOE_NVFP4_W4A16
+        ws = torch.empty(metis.metis_workspace_size(op, T, I, H, k, E), dtype=torch.uint8, device=dev)
+        if a.op == "moefew":
+            wu, wd = _codes(E * I, H, g).view(E, I, H), _codes(E * H, I, g).view(E, H, I)
+            su = torch.rand(E, I, device=dev, generator=g) * 1e-3
+            sd = torch.rand(E, H, device=dev, generator=g) * 1e-3
+            call = lambda: metis.metis_moe_w8a16(x, ids, w, wu, su, wd, sd, y, ws)
+        else:
+            wu = torch.randint(0, 256, (E, I, H // 2), dtype=torch.uint8, device=dev, generator=g)
+            wd = torch.randint(0, 256, (E, H, I // 2), dtype=torch.uint8, device=dev, generator=g)
+            sfu, sfd = _sf(E * I * H // 16, g), _sf(E * H * I // 16, g)
+            gu = torch.rand(E, device=dev, generator=g) * 1e-3 + 1e-4
+            gd = torch.rand(E, device=dev, generator=g) * 1e-3 + 1e-4
+            call = lambda: metis.metis_moe_nvfp4_w4a16(x, ids, w, wu, sfu, gu, wd, sfd, gd, y, ws)
+    elif a.op == "w4a16":
+        M, N, K = a.dims
+        x = torch.randn(M, K, device=dev, generator=g).to(torch.bfloat16)
+        qb = torch.randint(0, 256, (N, K // 2), dtype=torch.uint8, device=dev, generator=g)
+        sb = _sf(N * K // 16, g)
+        gb = torch.full((1,), 1e-3, device=dev)
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+        ws = torch.empty(metis.metis_workspace_size(metis.METIS_OP_NVFP4_W4A16, M, N, K), dtype=torch.uint8,
+                         device=dev)
+        call = lambda: metis.metis_nvfp4_w4a16_gemm(x, qb, sb, gb, y, ws)
+    elif a.op in ("quantmx", "gemmmx"):
+        M, K = a.dims[0], a.dims[-1]
+        N = a.dims[1] if a.op == "gemmmx" else 128
+        Mp = (M + 127) // 128 * 128
+        x = torch.randn(M, K, device=dev, generator=g).to(torch.bfloat16)
+        qa = torch.zeros(Mp, K // 2, dtype=torch.uint8, device=dev)
+        sa = torch.empty(Mp * K // 32, dtype=torch.uint8, device=dev)
+        if a.op == "quantmx":
+            back = torch.empty_like(x)
+
+            def call():
+                metis.metis_quant_mxfp4(x, qa[:M], sa, tiled=True)
+                metis.metis_dequant_mxfp4(qa[:M], sa, back, tiled=True)
+        else:
+            qb = torch.empty(N, K // 2, dtype=torch.uint8, device=dev)
+            sb = torch.empty(N * K // 32, dtype=torch.uint8, device=dev)
+            y = torch.empty(M, N, dtype=torch.bfloat16, device=dev)
+            metis.metis_quant_mxfp4(x, qa[:M], sa, tiled=True)
+            metis.metis_quant_mxfp4(torch.randn(N, K, device=dev, generator=g), qb, sb, tiled=True)
+            call = lambda: metis.metis_mxfp4_gemm(qa, sa, qb, sb, y)
     elif a.op == "bf16":
         M, N, K = a.dims
         x = torch.randn(M, K, device=dev, generator=g).to(torch.bfloat16)
