@@ -311,6 +311,61 @@ def test_w4a16_special_rows_capture_and_streams(metis, M):
     assert metis.metis_check_device_status() == 0
 
 
+@pytest.mark.parametrize("M", [2048, 2049, 2300])
+def test_w4a16_around_the_widening(metis, M):
+    """Past 2048 tokens the weights are widened into the workspace; the rows of both forms agree."""
+    N, K = 384, 1088
+    g = gen(650)
+    x = torch.randn(2300, K, generator=g, device="cuda").bfloat16()[:M]
+    q, sf, gs = nvfp4_weights(g, 1, N, K)
+    n = metis.metis_workspace_size(metis.METIS_OP_NVFP4_W4A16, M, N, K)
+    assert (n > 0) == (M > 2048)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") if n else None
+    y = torch.full((M + 1, N), NAN, dtype=torch.bfloat16, device="cuda")
+    metis.metis_nvfp4_w4a16_gemm(x, q[0], sf, gs, y[:M], ws)
+    assert metis.metis_check_device_status() == 0
+    assert_within(y[:M], *ref.product(x, ref.nvfp4_values(q, sf, gs)[0]))
+    assert bool(torch.isnan(y[M]).all())
+
+
+@by_format
+def test_moe_weights_past_32_bit_offsets(metis, fmt):
+    """More than 2^32 codes per projection, the chosen experts at both ends."""
+    T, H, I, E, k = 5, 2048, 2176, 1024, 3
+    chosen = torch.tensor([0, 1, 511, 1022, 1023], device="cuda")
+    g = gen(660)
+    pick = torch.rand(T, 5, generator=g, device="cuda").topk(k, dim=1).indices
+    small = layer(fmt, 661, T, H, I, 5, k, pick)
+    big = {**small, "E": E, "ids": chosen[pick].to(torch.int32).contiguous()}
+    for p in ("up", "down"):
+        big[p] = tuple(torch.zeros(E * (t.numel() // 5), dtype=t.dtype, device="cuda") for t in small[p])
+        big[p] = tuple(t.view(E, *u.shape[1:]) if u.shape[0] == 5 else t for t, u in zip(big[p], small[p]))
+        for dst, src in zip(big[p], small[p]):
+            dst.view(E, -1)[chosen] = src.view(5, -1)
+    y = run(metis, fmt, big)
+    assert metis.metis_check_device_status() == 0
+    assert_within(y, *expect(fmt, small))
+
+
+@by_format
+def test_no_tokens(metis, fmt):
+    d = layer(fmt, 670, 0, 256, 128, 4, 2, torch.empty(0, 2, device="cuda"))
+    assert run(metis, fmt, d, torch.empty(0, dtype=torch.uint8, device="cuda")).shape == (0, 256)
+    q, sf, gs = nvfp4_weights(gen(671), 1, 128, 64)
+    metis.metis_nvfp4_w4a16_gemm(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), q[0], sf, gs,
+                                 torch.empty(0, 128, dtype=torch.bfloat16, device="cuda"))
+    assert metis.metis_check_device_status() == 0
+
+
+@pytest.mark.parametrize("argv", [["moefew", "3"], ["moe4few", "40"], ["w4a16", "5", "256", "192"],
+                                  ["w4a16", "70", "256", "192"], ["quantmx", "9", "256"], ["gemmmx", "9", "256", "384"]],
+                         ids=lambda a: "-".join(a))
+def test_drive_commands(metis, argv, capsys):
+    from moe_gemm_token_b200 import drive
+    assert drive.main([*argv, "--calls", "2"]) == 0
+    assert "device status 0" in capsys.readouterr().out
+
+
 @by_format
 def test_moe_binding_refuses_what_the_library_cannot_see(metis, fmt):
     d = layer(fmt, 800, 4, 256, 128, 4, 2)

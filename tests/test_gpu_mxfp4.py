@@ -196,6 +196,35 @@ def test_layer_quantised_end_to_end_captured_and_replayed(metis):
     assert torch.equal(y, want) and metis.metis_check_device_status() == 0
 
 
+def test_rows_past_32_bit_offsets(metis):
+    """More than 2^32 bytes of x and 2^32 codes; checked at both ends."""
+    R, K = 65600, 65536
+    x = torch.zeros(R, K, dtype=torch.bfloat16, device="cuda")
+    ends = torch.cat((torch.arange(40), torch.arange(R - 90, R))).cuda()
+    x[ends] = torch.randn(ends.numel(), K, generator=gen(90), device="cuda").bfloat16()
+    q = torch.empty(R, K // 2, dtype=torch.uint8, device="cuda")
+    sf = torch.empty((R + 127) // 128 * 128 * K // 32, dtype=torch.uint8, device="cuda")
+    metis.metis_quant_mxfp4(x, q, sf, tiled=True)
+    want, c, _ = ref.mxfp4_quant(x[ends])
+    atoms = K // 128 * 512
+    r = ends.unsqueeze(1)
+    b = torch.arange(K // 32, device="cuda").unsqueeze(0)
+    assert torch.equal(sf[(r // 128) * atoms + b // 4 * 512 + 16 * (r % 32) + 4 * (r % 128 // 32) + b % 4], c)
+    x.fill_(float("nan"))
+    metis.metis_dequant_mxfp4(q, sf, x, tiled=True)
+    assert torch.equal(x[ends].double(), want)
+    assert bool((x[1000:1100] == 0).all()) and metis.metis_check_device_status() == 0
+
+
+def test_no_rows(metis):
+    def empty(*shape, dtype=torch.uint8):
+        return torch.empty(*shape, dtype=dtype, device="cuda")
+    metis.metis_quant_mxfp4(empty(0, 128, dtype=torch.bfloat16), empty(0, 64), empty(0))
+    metis.metis_dequant_mxfp4(empty(0, 64), empty(0), empty(0, 128, dtype=torch.bfloat16))
+    metis.metis_mxfp4_gemm(empty(0, 64), empty(0), empty(128, 64), empty(512), empty(0, 128, dtype=torch.bfloat16))
+    assert metis.metis_check_device_status() == 0
+
+
 def test_binding_refuses_what_the_library_cannot_see(metis):
     x = torch.zeros(4, 256, dtype=torch.bfloat16, device="cuda")
     q = torch.zeros(4, 128, dtype=torch.uint8, device="cuda")
