@@ -180,9 +180,9 @@ METIS_API int metis_moe_nvfp4_w4a16(const void* x_bf16, const int32_t* topk_ids,
  *   x [M, K] BF16 (dense rows); qb, sfb, gb as in metis_nvfp4_gemm.
  * K a multiple of 64 in [64, 65536], N a multiple of 128 up to 2^20, M >= 0;
  * x, codes, tiled scales and y 16-byte aligned; y overlaps no other argument.
- * Up to 16 tokens the weights are streamed past them as in the layer above (x
- * keeps its BF16 values, elements below 2^-29 of a token's largest magnitude
- * lose bits); beyond, they are multiplied as BF16.
+ * Up to 16 tokens the weights may be streamed past them as in the layer above
+ * (x keeps its BF16 values, elements below 2^-29 of a token's largest
+ * magnitude lose bits); otherwise they are multiplied as BF16.
  *   workspace  metis_workspace_size(METIS_OP_NVFP4_W4A16, M, N, K, 0, 0)
  *              bytes, 256-byte aligned: 0 (NULL allowed) up to 2048 tokens;
  *              beyond, the widened weights. Overwritten: calls that may

@@ -80,9 +80,15 @@ int launch_w8a16_tensor(const __nv_bfloat16* x, const uint8_t* wq, const float* 
                         __nv_bfloat16* y, int M, int N, int K, cudaStream_t st);
 
 // NVFP4 weight-only GEMM on the tensor cores (w16_gemm.cu), weights widened
-// in the kernel; arguments validated by the caller.
-int launch_nvfp4_w4a16_tensor(const __nv_bfloat16* x, const uint8_t* q, const uint8_t* sf, const float* g,
-                              __nv_bfloat16* y, int M, int N, int K, cudaStream_t st);
+// in the kernel: how it would run (tokens per tile, CTAs per tile, tiles,
+// stages of a CTA), and the launch; arguments validated by the caller.
+struct W4a16Plan {
+    int tm, ks;
+    int64_t tiles, stages;
+};
+int plan_nvfp4_w4a16_tensor(int M, int N, int K, W4a16Plan* plan);
+int launch_nvfp4_w4a16_tensor(const W4a16Plan& plan, const __nv_bfloat16* x, const uint8_t* q, const uint8_t* sf,
+                              const float* g, __nv_bfloat16* y, int M, int N, int K, cudaStream_t st);
 
 // Per-row E4M3 quantizer (quant.cu), for T = __nv_bfloat16 or float; the
 // arguments are validated by the caller. dst_rows non-null: row r's codes

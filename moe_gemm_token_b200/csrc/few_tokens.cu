@@ -1096,16 +1096,29 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
 }  // namespace few
 
 // metis_nvfp4_w4a16_gemm by its tokens, measured on B200 (us; N x K):
-//                        6144x2048   14336x4096   2048x8192
-//    16  stream              10.5        20.5        15.1
-//        tensor cores        12.8        22.2        38.3
-//    32  stream              21.6        52.5           -
-//        tensor cores        12.8        22.3        38.5
-//  2048  tensor cores        48.5           -           -
-//        widened first       50.7           -           -
-//  4096  tensor cores        92.2           -           -
-//        widened first       82.4           -           -
+//                        6144x2048   14336x4096   2048x6144   1024x1024   4096x14336
+//     1  streamed             5.4        11.1         5.1         3.6        12.3
+//        tensor cores         9.2        22.5         9.5         4.3        20.9
+//     8  streamed             7.0        13.9        10.0         4.0        30.7
+//        tensor cores         9.4        22.5         9.6         4.5        21.0
+//    16  streamed             8.8        19.1        13.9         5.1        56.2
+//        tensor cores         9.3        22.2         9.7         4.6        21.2
+//    32  streamed            21.6        52.5
+//        tensor cores         9.8        22.3
+//  2048  tensor cores        48.5
+//        widened first       50.7
+//  4096  tensor cores        92.2
+//        widened first       82.4
 constexpr int64_t kStreamTokens = 16, kWidenTokens = 2048;
+
+// Up to kStreamTokens, by estimates fitted to the table, in ns: 3000 + 100 per
+// 1024 staged operand values + the codes at 3.2 TB/s, against 4000 + 600 per
+// stage. The stream's operand has to fit shared memory in one piece.
+static bool nvfp4_w4a16_streams(int64_t M, int64_t N, int64_t K, const W4a16Plan& plan) {
+    const int64_t staged = (M <= 8 ? M : kStreamTokens) * K;
+    return M <= kStreamTokens && (M == 1 || (M <= 8 ? M : 8) * K <= 80 * 1024) &&
+           staged * 100 / 1024 + N * K / 6400 < 1000 + 600 * plan.stages;
+}
 
 size_t nvfp4_w4a16_workspace(int64_t M, int64_t N, int64_t K) {
     return M <= kWidenTokens ? 0 : static_cast<size_t>(few::align256(2 * N * K) + few::align256(4 * N));
@@ -1195,10 +1208,14 @@ extern "C" int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, con
     int rc = current_device_info(&di);
     if (rc) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (M > kStreamTokens && M <= kWidenTokens)
-        return launch_nvfp4_w4a16_tensor(static_cast<const __nv_bfloat16*>(x_bf16), qb, sfb, gb,
-                                         static_cast<__nv_bfloat16*>(y_bf16), static_cast<int>(M), static_cast<int>(N),
-                                         static_cast<int>(K), st);
+    if (M <= kWidenTokens) {
+        W4a16Plan plan;
+        if ((rc = plan_nvfp4_w4a16_tensor(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), &plan))) return rc;
+        if (!nvfp4_w4a16_streams(M, N, K, plan))
+            return launch_nvfp4_w4a16_tensor(plan, static_cast<const __nv_bfloat16*>(x_bf16), qb, sfb, gb,
+                                             static_cast<__nv_bfloat16*>(y_bf16), static_cast<int>(M), static_cast<int>(N),
+                                             static_cast<int>(K), st);
+    }
     if (M > kWidenTokens) {
         // many tokens: widen the weights once, then the BF16 CTA-pair GEMM
         __nv_bfloat16* wide = static_cast<__nv_bfloat16*>(workspace);

@@ -38,7 +38,9 @@
 // thread reads 32 code bytes and one word of four block scales per stage, PF
 // = 8 stages ahead, and widens D2(q) D(sf) exactly (FP16 product, six
 // significant bits); the epilogue applies the one global scale. Tiles of 32
-// and 64 tokens keep the MMAs of few tokens short (N = 32 or 64).
+// and 64 tokens keep the MMAs of few tokens short (N = 32 or 64). What bounds
+// a CTA is the issue of the MMAs (8 a stage of 0.55 us, whatever N up to
+// 128), so a tile's K is split over a cluster while SMs are free (SPLIT).
 #include "common.cuh"
 
 namespace metis {
@@ -85,6 +87,7 @@ struct Params {
     const uint8_t* sf;    // FP4: tiled block scales
     __nv_bfloat16* y;     // [M, N]
     int M, N, K;
+    int ks;               // SPLIT: CTAs (a cluster) that share the K of a tile
     uint32_t* status;
     uint64_t timeout_ns;
 };
@@ -151,7 +154,22 @@ __device__ __forceinline__ void nvfp4x16_to_bf16(uint32_t w0, uint32_t w1, uint3
     }
 }
 
-template <int TM, bool FP4 = false>
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+constexpr int MAX_KS = 8;  // a portable cluster
+
+// SPLIT: one tile per cluster of p.ks CTAs, each multiplying its part of K.
+// The partial sums (FP32) meet through distributed shared memory: every CTA
+// leaves its own in its ring, which all its MMAs have read by then, and adds
+// up a share of the tokens in the order of K.
+template <int TM, bool FP4 = false, bool SPLIT = false>
 __global__ void __launch_bounds__(THREADS, 1)
 w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
     using C = Cfg<TM>;
@@ -204,6 +222,10 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
     const int num_m = (p.M + TM - 1) / TM;
     const int total = num_m * ((p.N + TILE_N - 1) / TILE_N);
     const int num_kb = (p.K + BKE - 1) / BKE;
+    const int rank = SPLIT ? static_cast<int>(blockIdx.x) % p.ks : 0;
+    const int t_first = SPLIT ? static_cast<int>(blockIdx.x) / p.ks : static_cast<int>(blockIdx.x);
+    const int t_step = SPLIT ? total : static_cast<int>(gridDim.x);
+    const int kb_first = SPLIT ? rank * num_kb / p.ks : 0, kb_end = SPLIT ? (rank + 1) * num_kb / p.ks : num_kb;
     // tiles: token block fastest, so CTAs running together share weight rows
 
     if (warp == 0) {
@@ -211,9 +233,9 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
             // ------------------------------------------------------- producer
             int s = 0;
             uint32_t ph = 0;
-            for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x) {
+            for (int t = t_first; t < total && !*abort_flag; t += t_step) {
                 const int m0 = (t % num_m) * TM;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb_first; kb < kb_end; ++kb) {
                     if (!mbar_wait(empty(s), ph ^ 1u, p.timeout_ns, p.status)) {
                         *abort_flag = 1;
                         break;
@@ -238,7 +260,7 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
             uint32_t ph = 0;
             int acc = 0;
             uint32_t acc_ph = 0;
-            for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x) {
+            for (int t = t_first; t < total && !*abort_flag; t += t_step) {
                 if (!mbar_wait(tempty(acc), acc_ph ^ 1u, p.timeout_ns, p.status)) {
                     *abort_flag = 1;
                     break;
@@ -246,7 +268,7 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
                 tc_fence_after();
                 const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc * TM);
                 bool ok = true;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb_first; kb < kb_end; ++kb) {
                     if (!mbar_wait(full(s), ph, p.timeout_ns, p.status)) {
                         ok = false;
                         break;
@@ -258,7 +280,7 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
                     // K = 16 per MMA: 8 TMEM columns of A, 32 bytes along a box row of B
 #pragma unroll
                     for (int k = 0; k < BOXE / 16; ++k)
-                        mma_f16_tmem_a(d_tmem, a_tmem + 8 * k, bdesc0 + 2 * k, C::IDESC, (kb > 0 || k > 0) ? 1u : 0u);
+                        mma_f16_tmem_a(d_tmem, a_tmem + 8 * k, bdesc0 + 2 * k, C::IDESC, (kb > kb_first || k > 0) ? 1u : 0u);
 #pragma unroll
                     for (int k = 0; k < BOXE / 16; ++k)
                         mma_f16_tmem_a(d_tmem, a_tmem + 8 * (k + BOXE / 16), bdesc1 + 2 * k, C::IDESC, 1u);
@@ -283,7 +305,7 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
         const bool wide = (p.K % 32) == 0 && (reinterpret_cast<uintptr_t>(p.w) & 31u) == 0;
         int s = 0;
         uint32_t ph = 0;
-        for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x) {
+        for (int t = t_first; t < total && !*abort_flag; t += t_step) {
             const int row = (t / num_m) * TILE_N + lane_base + lane;  // weight row = output channel
             const bool row_ok = row < p.N;
             const size_t row_bytes = FP4 ? p.K / 2 : p.K;
@@ -298,7 +320,7 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
             // through L1), 16-byte loads otherwise and at the end of K
             auto load_fp4 = [&](int kb, uint4 (&r)[4]) {
                 r[0] = r[1] = r[2] = make_uint4(0, 0, 0, 0);
-                if (row_ok && kb * BKE + 64 * half < p.K) {
+                if (row_ok && kb < kb_end && kb * BKE + 64 * half < p.K) {
                     // one 32-byte load touches each of the warp's 32 rows once
                     if (wide) {
                         ld_w32(wrow + kb * (BKE / 2), r[0], r[1]);
@@ -332,13 +354,13 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
             // PF stages of weight bytes in flight per thread (L2 latency)
             uint4 buf[PF][4];
 #pragma unroll
-            for (int d = 0; d < PF; ++d) load_kb(d, buf[d]);
+            for (int d = 0; d < PF; ++d) load_kb(kb_first + d, buf[d]);
             bool ok = true;
-            for (int kb0 = 0; kb0 < num_kb && ok; kb0 += PF) {
+            for (int kb0 = kb_first; kb0 < kb_end && ok; kb0 += PF) {
 #pragma unroll
                 for (int d = 0; d < PF; ++d) {
                     const int kb = kb0 + d;
-                    if (kb >= num_kb || !ok) break;
+                    if (kb >= kb_end || !ok) break;
                     uint32_t words[32];
                     if constexpr (FP4) {
                         const uint32_t sc = buf[d][2].x;
@@ -381,7 +403,7 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
         uint8_t* stg = staging + (warp - 2 - CONV_WARPS) * 2048;  // [32 tokens][32 channels] BF16
         int acc = 0;
         uint32_t acc_ph = 0;
-        for (int t = blockIdx.x; t < total && !*abort_flag; t += gridDim.x) {
+        for (int t = t_first; t < total && !*abort_flag; t += t_step) {
             const int m0 = (t % num_m) * TM;
             const int n_lane = (t / num_m) * TILE_N + q * 32 + lane;  // this thread's channel
             const float sw = n_lane < p.N ? p.s_w[FP4 ? 0 : n_lane] : 0.0f;
@@ -402,6 +424,12 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(tempty(acc));
+                }
+                if constexpr (SPLIT) {
+                    float* part = reinterpret_cast<float*>(ring) + c * 32 * TILE_N + q * 32 + lane;  // [token][channel]
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) part[j * TILE_N] = __uint_as_float(v[j]);
+                    continue;
                 }
                 // lane = channel, j = token: transpose into [token][channel]
                 __syncwarp();
@@ -427,11 +455,37 @@ w16_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const Params p) {
     }
 
     __syncwarp();
+    if constexpr (SPLIT) {
+        cluster_sync_all();  // all partial sums are in place
+        const int m0 = (t_first % num_m) * TM, tokens = min(TM, p.M - m0);
+        const int n = (t_first / num_m) * TILE_N + 4 * lane;
+        const float sw = p.s_w[0];
+        // a warp adds up a token's 128 channels
+        for (int i = rank + p.ks * warp; i < tokens; i += p.ks * (THREADS / 32)) {
+            const uint32_t at = smem_u32(ring) + static_cast<uint32_t>((i * TILE_N + 4 * lane) * 4);
+            float4 v[MAX_KS];
+#pragma unroll
+            for (int r = 0; r < MAX_KS; ++r)
+                if (r < p.ks) v[r] = ld_cluster(mapa_shared(at, r));
+            float4 a = v[0];
+#pragma unroll
+            for (int r = 1; r < MAX_KS; ++r)
+                if (r < p.ks) a.x += v[r].x, a.y += v[r].y, a.z += v[r].z, a.w += v[r].w;
+            *reinterpret_cast<uint2*>(p.y + static_cast<size_t>(m0 + i) * p.N + n) =
+                make_uint2(pack_bf16x2(__fmul_rn(a.x, sw), __fmul_rn(a.y, sw)),
+                           pack_bf16x2(__fmul_rn(a.z, sw), __fmul_rn(a.w, sw)));
+        }
+        __syncwarp();
+    }
     tc_fence_before();
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_sync_all();  // the others have read this CTA's partial sums
     }
 }
 
@@ -461,7 +515,7 @@ int launch_w8a16_tensor(const __nv_bfloat16* x, const uint8_t* wq, const float* 
     if (rc) return rc;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status))) return rc;
-    Params p{wq, s_w, nullptr, y, M, N, K, status, watchdog_ns()};
+    Params p{wq, s_w, nullptr, y, M, N, K, 1, status, watchdog_ns()};
     // a wave of 256-token tiles takes about 1.25 times as long as one of
     // 128-token tiles (17.7 against 14.0 us for 6144 x 2048 weights) for
     // twice the work (the same MMA count, the epilogue not overlapped): take
@@ -486,48 +540,105 @@ int launch_w8a16_tensor(const __nv_bfloat16* x, const uint8_t* wq, const float* 
                       "w8a16 tensor-core GEMM launch");
 }
 
-// NVFP4 weight-only GEMM on the tensor cores (arguments validated by the
-// caller): x BF16 [M, K], codes [N, K/2], tiled scales, N % 128 == 0, K % 64 == 0.
-int launch_nvfp4_w4a16_tensor(const __nv_bfloat16* x, const uint8_t* q, const uint8_t* sf, const float* g,
-                              __nv_bfloat16* y, int M, int N, int K, cudaStream_t st) {
-    using namespace w16;
-    DeviceInfo di;
-    int rc = current_device_info(&di);
-    if (rc) return rc;
-    static std::atomic<uint64_t> attr_done[64];
-    rc = once_per_context(attr_done, di.device, [] {
+namespace w16 {
+
+// Clusters of so many CTAs of the split kernel that are resident at once (one CTA per SM for every TM).
+std::atomic<int> resident[64][MAX_KS + 1];
+
+int prepare_fp4(const DeviceInfo& di) {
+    static std::atomic<uint64_t> done[64];
+    return once_per_context(done, di.device, [&] {
         auto set = [](const void* f, size_t bytes) {
             return cuda_check(cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)),
                               "cudaFuncSetAttribute(w16 nvfp4)");
         };
-        int r = set(reinterpret_cast<const void*>(w16_gemm_kernel<32, true>), Cfg<32>::SMEM_BYTES);
-        if (!r) r = set(reinterpret_cast<const void*>(w16_gemm_kernel<64, true>), Cfg<64>::SMEM_BYTES);
-        if (!r) r = set(reinterpret_cast<const void*>(w16_gemm_kernel<128, true>), Cfg<128>::SMEM_BYTES);
-        if (!r) r = set(reinterpret_cast<const void*>(w16_gemm_kernel<256, true>), Cfg<256>::SMEM_BYTES);
+        auto both = [&](auto whole, auto split, size_t bytes) {
+            const int r = set(reinterpret_cast<const void*>(whole), bytes);
+            return r ? r : set(reinterpret_cast<const void*>(split), bytes);
+        };
+        int r = both(w16_gemm_kernel<32, true>, w16_gemm_kernel<32, true, true>, Cfg<32>::SMEM_BYTES);
+        if (!r) r = both(w16_gemm_kernel<64, true>, w16_gemm_kernel<64, true, true>, Cfg<64>::SMEM_BYTES);
+        if (!r) r = both(w16_gemm_kernel<128, true>, w16_gemm_kernel<128, true, true>, Cfg<128>::SMEM_BYTES);
+        if (!r) r = both(w16_gemm_kernel<256, true>, w16_gemm_kernel<256, true, true>, Cfg<256>::SMEM_BYTES);
+        for (int ks = 2; !r && ks <= MAX_KS; ++ks) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = ks;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(di.num_sms / ks * ks);
+            cfg.blockDim = dim3(THREADS);
+            cfg.dynamicSmemBytes = Cfg<256>::SMEM_BYTES;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            r = cuda_check(cudaOccupancyMaxActiveClusters(&n, w16_gemm_kernel<256, true, true>, &cfg),
+                           "cudaOccupancyMaxActiveClusters(w16 nvfp4)");
+            resident[di.device & 63][ks].store(n, std::memory_order_relaxed);
+        }
         return r;
     });
+}
+
+}  // namespace w16
+
+// The tile width and the split for an NVFP4 weight-only product, and the
+// stages (of 128 elements of K, 0.6 us each) that its CTAs do one after another.
+int plan_nvfp4_w4a16_tensor(int M, int N, int K, W4a16Plan* plan) {
+    using namespace w16;
+    DeviceInfo di;
+    int rc = current_device_info(&di);
+    if (rc || (rc = prepare_fp4(di))) return rc;
+    const int num_kb = (K + BKE - 1) / BKE;
+    auto make = [&](int tm) {
+        W4a16Plan w;
+        w.tm = tm;
+        w.tiles = static_cast<int64_t>((M + tm - 1) / tm) * (N / TILE_N);
+        // CTAs per tile: as many as are resident at once (37 tokens: 6144 x 2048
+        // 13.2 us with one, 9.9 with two; 2048 x 6144 30.6 with one, 10.2 with six;
+        // a second wave of clusters costs more than the split gains: 16.2 with three)
+        w.ks = num_kb < MAX_KS ? num_kb : MAX_KS;
+        while (w.ks > 1 && w.tiles > resident[di.device & 63][w.ks].load(std::memory_order_relaxed)) --w.ks;
+        w.stages = (w.tiles + di.num_sms - 1) / di.num_sms * ((num_kb + w.ks - 1) / w.ks);
+        return w;
+    };
+    *plan = make(M <= 32 ? 32 : M <= 64 ? 64 : 128);
+    if (M > 128) {
+        // a stage of 256 tokens takes 1.25 times as long; joining the partial
+        // sums costs about 2 stages, 5 with 256 tokens (256 tokens, 2048 x 6144:
+        // 128 wide 15.1 us, 256 wide 17.2; 14336 x 4096: 44.7 and 30.1)
+        const W4a16Plan w = make(256);
+        const int64_t wide = 5 * w.stages + (w.ks > 1 ? 20 : 0), narrow = 4 * plan->stages + (plan->ks > 1 ? 8 : 0);
+        if (wide < narrow) *plan = w;
+    }
+    return METIS_OK;
+}
+
+// NVFP4 weight-only GEMM on the tensor cores (arguments validated by the
+// caller): x BF16 [M, K], codes [N, K/2], tiled scales, N % 128 == 0, K % 64 == 0.
+int launch_nvfp4_w4a16_tensor(const W4a16Plan& plan, const __nv_bfloat16* x, const uint8_t* q, const uint8_t* sf,
+                              const float* g, __nv_bfloat16* y, int M, int N, int K, cudaStream_t st) {
+    using namespace w16;
+    DeviceInfo di;
+    int rc = current_device_info(&di);
     if (rc) return rc;
     uint32_t* status = nullptr;
     if ((rc = device_status_word(&status))) return rc;
-    Params p{q, g, sf, y, M, N, K, status, watchdog_ns()};
-    // the tile width as in launch_w8a16_tensor; narrow tiles for few tokens
-    const int64_t nn = (N + TILE_N - 1) / TILE_N;
-    const int64_t t128 = (M + 127) / 128 * nn, t256 = (M + 255) / 256 * nn;
-    const int64_t w128 = (t128 + di.num_sms - 1) / di.num_sms, w256 = (t256 + di.num_sms - 1) / di.num_sms;
-    const int tm = M <= 32 ? 32 : M <= 64 ? 64 : 125 * w256 < 100 * w128 ? 256 : 128;
+    Params p{q, g, sf, y, M, N, K, plan.ks, status, watchdog_ns()};
     CUtensorMap tx;
     if ((rc = make_tmap_2d(&tx, x, 2, static_cast<uint64_t>(K), static_cast<uint64_t>(M), static_cast<uint64_t>(K) * 2,
-                           BOXE, tm, true)))
+                           BOXE, plan.tm, true)))
         return rc;
-    const int64_t tiles = (M + tm - 1) / tm * nn;
-    const dim3 grid(static_cast<unsigned>(tiles < di.num_sms ? tiles : di.num_sms));
-    auto go = [&](auto kernel, size_t bytes) {
-        return cuda_check(launch_pdl(kernel, grid, dim3(THREADS), bytes, st, 1, tx, p), "nvfp4 w4a16 tensor-core GEMM launch");
+    const bool split = plan.ks > 1;
+    const dim3 grid(static_cast<unsigned>(split ? plan.tiles * plan.ks : plan.tiles < di.num_sms ? plan.tiles : di.num_sms));
+    auto go = [&](auto whole, auto parts, size_t bytes) {
+        return cuda_check(launch_pdl(split ? parts : whole, grid, dim3(THREADS), bytes, st, plan.ks, tx, p),
+                          "nvfp4 w4a16 tensor-core GEMM launch");
     };
-    if (tm == 32) return go(w16_gemm_kernel<32, true>, Cfg<32>::SMEM_BYTES);
-    if (tm == 64) return go(w16_gemm_kernel<64, true>, Cfg<64>::SMEM_BYTES);
-    if (tm == 128) return go(w16_gemm_kernel<128, true>, Cfg<128>::SMEM_BYTES);
-    return go(w16_gemm_kernel<256, true>, Cfg<256>::SMEM_BYTES);
+    if (plan.tm == 32) return go(w16_gemm_kernel<32, true>, w16_gemm_kernel<32, true, true>, Cfg<32>::SMEM_BYTES);
+    if (plan.tm == 64) return go(w16_gemm_kernel<64, true>, w16_gemm_kernel<64, true, true>, Cfg<64>::SMEM_BYTES);
+    if (plan.tm == 128) return go(w16_gemm_kernel<128, true>, w16_gemm_kernel<128, true, true>, Cfg<128>::SMEM_BYTES);
+    return go(w16_gemm_kernel<256, true>, w16_gemm_kernel<256, true, true>, Cfg<256>::SMEM_BYTES);
 }
 
 namespace w16 {
