@@ -634,6 +634,7 @@ struct GemmParams {
     const int32_t* offsets;   // grouped: [E + 1] first rows (multiples of 128); dense: null
     const int32_t* counts;    // grouped: [E] rows per group
     int M, N, K, E;
+    int ks;                   // SPLIT: CTAs (a cluster) that share the K of a tile
     uint32_t* status;
     uint64_t timeout_ns;
 };
@@ -739,12 +740,30 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&v)[32], int c, cons
     }
 }
 
-template <int CTAS, bool GROUPED, bool MX = false>
+// SPLIT (one CTA per tile otherwise, dense): one tile per cluster of p.ks
+// CTAs, each multiplying its part of K. The partial sums (FP32) meet through
+// distributed shared memory: every CTA leaves its own where its operand tiles
+// were, which all its MMAs have read by then, and adds up a share of the rows
+// in the order of K.
+constexpr int MAX_KS = 8;                    // a portable cluster
+constexpr int PART_PITCH = BN * 4 + 16;      // bytes per row of partial sums, 4 banks apart
+
+__device__ __forceinline__ float4 ld_cluster(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+template <int CTAS, bool GROUPED, bool MX = false, bool SPLIT = false>
 __global__ void __launch_bounds__(THREADS, 1)
 nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                   const __grid_constant__ CUtensorMap tmSFA, const __grid_constant__ CUtensorMap tmSFB,
                   const __grid_constant__ CUtensorMap tmY, const GemmParams p) {
     using L = Lay<CTAS, GROUPED, MX>;
+    static_assert(!SPLIT || (CTAS == 1 && !GROUPED && ROWS * PART_PITCH <= L::SFA_OFF), "partial sums over the operand tiles");
     constexpr int STAGES = L::STAGES, SFA_STAGE = L::SFA_STAGE, SFB_STAGE = L::SFB_STAGE;
     constexpr int CPA = Sf<MX>::CPA, ATOMS = Sf<MX>::ATOMS;
     extern __shared__ uint8_t smem_raw[];
@@ -871,8 +890,12 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     const int kch_total = p.K / 64;             // 64-element chunks per row
     const int num_kb = (kch_total + KCH - 1) / KCH;
     const int atoms_total = kch_total / CPA;    // scale atoms per 128 rows
-    const int first = CTAS == 2 ? static_cast<int>(blockIdx.x / 2) : static_cast<int>(blockIdx.x);
-    const int stride = CTAS == 2 ? static_cast<int>(gridDim.x / 2) : static_cast<int>(gridDim.x);
+    const int first = CTAS == 2 ? static_cast<int>(blockIdx.x / 2)
+                      : SPLIT   ? static_cast<int>(blockIdx.x) / p.ks
+                                : static_cast<int>(blockIdx.x);
+    const int stride = CTAS == 2 ? static_cast<int>(gridDim.x / 2) : SPLIT ? sc.total : static_cast<int>(gridDim.x);
+    const int krank = SPLIT ? static_cast<int>(blockIdx.x) % p.ks : 0;
+    const int kb_first = SPLIT ? krank * num_kb / p.ks : 0, kb_end = SPLIT ? (krank + 1) * num_kb / p.ks : num_kb;
 
     if (warp == 0) {
         if (lane == 0) {
@@ -888,7 +911,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 // otherwise its scale atoms repeat the first half's (the
                 // columns it feeds are never stored)
                 const int64_t rb_b1 = ti.n0 + ROWS < p.N ? rb_b0 + 1 : rb_b0;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb_first; kb < kb_end; ++kb) {
                     if (!mbar_wait(empty(stage), phase ^ 1u, p.timeout_ns, p.status)) {
                         *abort_flag = 1;
                         break;
@@ -951,7 +974,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
                 }
                 tc_fence_after();
                 bool ok = true;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb_first; kb < kb_end; ++kb) {
                     if ((GROUPED && !mbar_wait(landed(stage), phase, p.timeout_ns, p.status)) ||
                         !mbar_wait(full(stage), phase, p.timeout_ns, p.status)) {
                         ok = false;
@@ -967,7 +990,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
 #pragma unroll
                     for (int c = 0; c < KCH; ++c) {
                         if (c < nk) {
-                            const uint32_t acc = (kb > 0 || c > 0) ? 1u : 0u;
+                            const uint32_t acc = (kb > kb_first || c > 0) ? 1u : 0u;
                             if constexpr (CTAS == 2)
                                 mma_nvf4_pair<MX>(tmem_base, adesc + 2 * c, bdesc + 2 * c, L::idesc(c),
                                                   sfa_t + 4 * (c / CPA), sfb_t + 8 * (c / CPA), acc);
@@ -1007,7 +1030,7 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             uint32_t phase = 0;
             for (int t = first; t < sc.total && !*abort_flag; t += stride) {
                 bool ok = true;
-                for (int kb = 0; kb < num_kb; ++kb) {
+                for (int kb = kb_first; kb < kb_end; ++kb) {
                     if (!mbar_wait(landed(stage), phase, p.timeout_ns, p.status) ||
                         (GROUPED && !mbar_wait(sfree(stage), phase ^ 1u, p.timeout_ns, p.status))) {
                         ok = false;
@@ -1069,6 +1092,19 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
             tmem_ld_32x32b_x32(tbase, va);
             tmem_ld_32x32b_x32(tbase + 32, vb);
             tmem_ld_wait();
+            if constexpr (SPLIT) {
+                if (row < ti.row_end) {
+                    float4* part_row = reinterpret_cast<float4*>(smem + (q * 32 + lane) * PART_PITCH) + 16 * part;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        part_row[j] = make_float4(__uint_as_float(va[4 * j]), __uint_as_float(va[4 * j + 1]),
+                                                  __uint_as_float(va[4 * j + 2]), __uint_as_float(va[4 * j + 3]));
+                        part_row[8 + j] = make_float4(__uint_as_float(vb[4 * j]), __uint_as_float(vb[4 * j + 1]),
+                                                      __uint_as_float(vb[4 * j + 2]), __uint_as_float(vb[4 * j + 3]));
+                    }
+                }
+                break;  // one tile
+            }
             // the whole accumulator has been read by this warp: release it
             // (relaxed: a release would first wait for this warp's stores of
             // the previous tile, holding up the next tile's MMAs)
@@ -1087,12 +1123,38 @@ nvfp4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant
     }
 
     __syncwarp();
+    if constexpr (SPLIT) {
+        cluster_sync_all();  // all partial sums are in place
+        const Tile ti = sc.get(first);
+        const int rows = min(ROWS, ti.row_end - ti.a_row0);
+        // a warp adds up 128 columns of a row
+        const int units = rows * (ti.n0 + 128 < p.N ? 2 : 1);
+        for (int u = krank + p.ks * warp; u < units; u += p.ks * (THREADS / 32)) {
+            const int i = u % rows, col = u / rows * 128 + 4 * lane;
+            const uint32_t at = smem_u32(smem) + static_cast<uint32_t>(i * PART_PITCH + col * 4);
+            float4 v[MAX_KS];
+#pragma unroll
+            for (int r = 0; r < MAX_KS; ++r)
+                if (r < p.ks) v[r] = ld_cluster(mapa_shared(at, r));
+            float4 a = v[0];
+#pragma unroll
+            for (int r = 1; r < MAX_KS; ++r)
+                if (r < p.ks) a.x += v[r].x, a.y += v[r].y, a.z += v[r].z, a.w += v[r].w;
+            *reinterpret_cast<uint2*>(p.y + static_cast<int64_t>(ti.a_row0 + i) * p.N + ti.n0 + col) =
+                make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+        }
+        __syncwarp();
+    }
     tc_fence_before();
     if constexpr (CTAS == 2) cluster_sync_all(); else __syncthreads();
     if (warp == 1) {
         tc_fence_after();
         if constexpr (CTAS == 2) tmem_dealloc_pair(tmem_base, TMEM_COLS);
         else tmem_dealloc(tmem_base, TMEM_COLS);
+    }
+    if constexpr (SPLIT) {
+        __syncwarp();
+        cluster_sync_all();  // the others have read this CTA's partial sums
     }
 }
 
@@ -1137,6 +1199,37 @@ int max_pairs(const DeviceInfo& di, int* out) {
     return METIS_OK;
 }
 
+// Clusters of ks CTAs of the split kernel that are resident at once.
+int split_clusters(const DeviceInfo& di, int ks, int* out) {
+    static std::atomic<uint64_t> done[64];
+    static std::atomic<int> resident[64][MAX_KS + 1];
+    using Kernel = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, GemmParams);
+    const int rc = once_per_context(done, di.device, [&] {
+        constexpr size_t smem = Lay<1, false, true>::BYTES;
+        const Kernel kernel = nvfp4_gemm_kernel<1, false, true, true>;
+        int r = cuda_check(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)),
+                           "cudaFuncSetAttribute(mxfp4 gemm)");
+        for (int k = 2; !r && k <= MAX_KS; ++k) {
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = k;
+            attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(di.num_sms / k * k);
+            cfg.blockDim = dim3(THREADS);
+            cfg.dynamicSmemBytes = smem;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int n = 0;
+            r = cuda_check(cudaOccupancyMaxActiveClusters(&n, kernel, &cfg), "cudaOccupancyMaxActiveClusters(mxfp4)");
+            resident[di.device & 63][k].store(n, std::memory_order_relaxed);
+        }
+        return r;
+    });
+    *out = resident[di.device & 63][ks].load(std::memory_order_relaxed);
+    return rc;
+}
+
 }  // namespace nvfp4
 
 // y = NVFP4 GEMM. a_rows: rows of A's code buffer (a multiple of 128);
@@ -1169,9 +1262,30 @@ static int launch_fp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* g
     if ((rc = device_status_word(&p.status))) return rc;
     p.timeout_ns = watchdog_ns();
     const bool grouped = offsets != nullptr;
-    const bool pair = grouped || M > ROWS;
+    bool pair = grouped || M > ROWS;
+    const int64_t tiles = ((static_cast<int64_t>(M) + ROWS - 1) / ROWS) * ((N + BN - 1) / BN);
+    if constexpr (MX) {
+        // Few tiles: their K over a cluster, as many CTAs as are resident at
+        // once. A k-block takes 0.4 us; joining the partial sums takes as long
+        // as 2 of them and one more per 16 rows (us, N x K, whole and split:
+        // 16 rows 2048 x 6144 14.2 and 6.6, 6144 x 2048 7.5 and 6.3; 100 rows
+        // 2048 x 6144 14.5 and 10.6, 2048 x 2048 7.5 and 9.7).
+        const int num_kb = (K / 64 + KCH - 1) / KCH;
+        int ks = num_kb < MAX_KS ? num_kb : MAX_KS;
+        for (; ks > 1; --ks) {
+            int n = 0;
+            if ((rc = split_clusters(di, ks, &n))) return rc;
+            if (tiles <= n) break;
+        }
+        const int blocks = (num_kb + ks - 1) / ks;   // k-blocks of a CTA
+        const int join = 2 + ((M < ROWS ? M : ROWS) + 15) / 16;
+        if (ks > 1 && 10 * (blocks + join) < 9 * num_kb) {
+            p.ks = (num_kb + blocks - 1) / blocks;
+            pair = false;
+        }
+    }
     const uint32_t b_box = pair ? BN / 2 : BN;
-    CUtensorMap ta, tb, tsa, tsb, ty;
+    CUtensorMap ta, tb, ty, tsa{}, tsb{};   // the scales through TMA: CTA pairs only
     // y: [M, N] (dense) or one row per row of A (grouped), BF16
     if ((rc = make_tmap_2d_sw64(&ty, y, 2, static_cast<uint64_t>(N), static_cast<uint64_t>(grouped ? a_rows : M),
                                 static_cast<uint64_t>(N) * 2, 32, 32)))
@@ -1183,10 +1297,10 @@ static int launch_fp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* g
                            static_cast<uint64_t>(K / 2), BKB, b_box, true)))
         return rc;
     // the tiled scales as rows of 256 bytes (two per atom), a k-block's atoms per box
-    if ((rc = make_tmap_2d(&tsa, sfa, 1, SF_ROW, static_cast<uint64_t>(a_rows) * (K / SF_BLOCK) / SF_ROW, SF_ROW,
+    if (pair && (rc = make_tmap_2d(&tsa, sfa, 1, SF_ROW, static_cast<uint64_t>(a_rows) * (K / SF_BLOCK) / SF_ROW, SF_ROW,
                            SF_ROW, BOX, false)))
         return rc;
-    if ((rc = make_tmap_2d(&tsb, sfb, 1, SF_ROW, static_cast<uint64_t>(b_rows) * (K / SF_BLOCK) / SF_ROW, SF_ROW,
+    if (pair && (rc = make_tmap_2d(&tsb, sfb, 1, SF_ROW, static_cast<uint64_t>(b_rows) * (K / SF_BLOCK) / SF_ROW, SF_ROW,
                            SF_ROW, BOX, false)))
         return rc;
     if (pair) {
@@ -1208,8 +1322,12 @@ static int launch_fp4_gemm(const uint8_t* qa, const uint8_t* sfa, const float* g
                                      Lay<2, false, MX>::BYTES, st, 2, ta, tb, tsa, tsb, ty, p),
                           "nvfp4 gemm (CTA pair) launch");
     }
-    const int64_t tiles = ((static_cast<int64_t>(M) + ROWS - 1) / ROWS) * ((N + BN - 1) / BN);
     if (tiles == 0) return METIS_OK;
+    if constexpr (MX)
+        if (p.ks > 1)
+            return cuda_check(launch_pdl(nvfp4_gemm_kernel<1, false, true, true>, dim3(static_cast<unsigned>(tiles * p.ks)),
+                                         dim3(THREADS), Lay<1, false, true>::BYTES, st, p.ks, ta, tb, tsa, tsb, ty, p),
+                              "mxfp4 gemm (split) launch");
     const int grid = static_cast<int>(tiles < di.num_sms ? tiles : di.num_sms);
     if ((rc = prepare_gemm<1, false, MX>(di))) return rc;
     return cuda_check(launch_pdl(nvfp4_gemm_kernel<1, false, MX>, dim3(grid), dim3(THREADS), Lay<1, false, MX>::BYTES,

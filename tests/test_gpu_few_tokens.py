@@ -267,7 +267,7 @@ def test_moe_router_to_layer_to_projection(metis):
 
 @pytest.mark.parametrize("N,K", [(128, 64), (256, 192), (384, 2048), (128, 8192), (256, 12352), (128, 65536),
                                  (2176, 4096), (6144, 320)])
-@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 37, 64, 65, 129, 300])
+@pytest.mark.parametrize("M", [1, 2, 7, 8, 9, 16, 17, 37, 64, 65, 129, 256, 300])
 def test_w4a16_sizes(metis, M, N, K):
     g = gen(600 + M + N)
     x = torch.randn(M, K, generator=g, device="cuda").bfloat16()

@@ -122,7 +122,8 @@ def mx_values(q, sf, R, K):
 
 
 GEMM = [(1, 128, 128), (16, 256, 256), (17, 384, 640), (127, 128, 2048), (128, 512, 384), (129, 256, 128),
-        (257, 1152, 896), (700, 2176, 1024), (3, 128, 65536), (300, 128, 8320)]
+        (257, 1152, 896), (700, 2176, 1024), (3, 128, 65536), (300, 128, 8320),
+        (5, 2048, 6144), (100, 384, 4224), (128, 1280, 8192), (129, 640, 6016), (500, 2048, 6144)]
 
 
 @pytest.mark.parametrize("M,N,K", GEMM)
