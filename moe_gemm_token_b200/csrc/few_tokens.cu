@@ -240,6 +240,12 @@ struct Chunk<__nv_bfloat16> {
             v[2 * i + 1] = bf16_hi(u[i]);
         }
     }
+    // bits of the largest magnitude, as binary32
+    __device__ __forceinline__ uint32_t amax() const {
+        const uint32_t m = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                                    __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+        return max(m & 0xFFFF0000u, m << 16);
+    }
 };
 template <>
 struct Chunk<float> {
@@ -251,6 +257,14 @@ struct Chunk<float> {
     __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+    __device__ __forceinline__ uint32_t amax() const {
+        float f[8];
+        get(f);
+        uint32_t m = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7FFFFFFFu);
+        return m;
     }
 };
 constexpr int STAGE_U = 4;  // chunks of a lane in flight
@@ -296,12 +310,7 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
         for (int q = q0; q < chunks; q += STAGE_U * step) {
             if (!loaded) load_chunks(v, row, q, step, chunks);
 #pragma unroll
-            for (int u = 0; u < STAGE_U; ++u) {
-                float f[8];
-                v[u].get(f);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7FFFFFFFu);
-            }
+            for (int u = 0; u < STAGE_U; ++u) m = max(m, v[u].amax());
         }
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) atomicMax(amax + i, m);
@@ -326,9 +335,13 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
                 float f[8];
                 v[u].get(f);
                 uint32_t h[4];
+                if (sa != sh) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) f[k] *= fb;
+                }
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const __half2 p = __floats2half2_rn(f[2 * k] * fa * fb, f[2 * k + 1] * fa * fb);
+                    const __half2 p = __floats2half2_rn(f[2 * k] * fa, f[2 * k + 1] * fa);
                     h[k] = *reinterpret_cast<const uint32_t*>(&p);
                 }
                 // past K: zeros (a second batch there is not what the lane kept)
