@@ -30,6 +30,11 @@
 //    through programmatic dependent launch, where an SM has room for both.
 //
 // Sums are added in a fixed order and no result depends on an atomic's order.
+//
+// With few weights per SM every instruction before the stream runs once, out
+// of a cold instruction cache: the code there is kept short (loops not
+// unrolled, tails left by `break` instead of predicated), which took a call of
+// one token from 13.6 to 13.0 us (FP8) and from 12.7 to 12.1 (NVFP4).
 #include <type_traits>
 
 #include "common.cuh"
@@ -59,12 +64,14 @@ enum Mode { UP = 0, DOWN = 1, OWN = 2, DENSE = 3 };
 // kernel, whose prologue then overlaps (few weights per SM: latency); 16 take
 // an SM by themselves and share one staged operand (many weights per SM).
 // DEPTH: pieces (2 KB) in flight per warp. 8 warps: OWN shares the SM with the
-// up-projection and reads 5 of its pieces ahead while that one runs. 16 warps,
-// us per call: FP8, 32 tokens 2 pieces 57.0, 3 pieces 56.4; NVFP4, which its
+// up-projection and reads its pieces ahead while that one runs (FP8, 1 token,
+// UP 4 and OWN 5 pieces 12.95 us a call, 3 and 5 13.1, 3 and 6 13.4, 2 and 5
+// 14.2; NVFP4 3 pieces 12.07, 4 pieces 12.17, 5 pieces 14.6). 16 warps, us per
+// call: FP8, 32 tokens 2 pieces 57.0, 3 pieces 56.4; NVFP4, which its
 // widening instructions bound, 64 tokens 2 pieces 28.3, 3 pieces 29.2.
 template <int FMT, int MODE, int GMAX, int W>
 struct Cta {
-    static constexpr int DEPTH = W == 8     ? (FMT == NVFP4 ? 4 : MODE == OWN ? 5 : MODE == UP ? 3 : 4)
+    static constexpr int DEPTH = W == 8     ? (FMT == NVFP4 ? 3 : MODE == OWN ? 5 : 4)
                                  : FMT == FP8 ? 3
                                               : 2;
 };
@@ -225,13 +232,18 @@ __device__ __forceinline__ int operand_chunk(int q) {
 // pitch. W / n' warps share a row (n' = n rounded up to a power of two), so
 // that a few rows are read with one round trip, and a lane keeps its chunks
 // in registers between the two steps (largest magnitude, shift) when they fit.
+// The largest magnitude of three, NaN if one of them is NaN.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float m;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+    return m;
+}
 template <typename In>
 struct Chunk;  // eight elements as loaded
 template <>
 struct Chunk<__nv_bfloat16> {
     uint4 w;
     __device__ __forceinline__ void load(const __nv_bfloat16* p) { w = *reinterpret_cast<const uint4*>(p); }
-    __device__ __forceinline__ void zero() { w = make_uint4(0, 0, 0, 0); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -254,17 +266,11 @@ struct Chunk<float> {
         a = *reinterpret_cast<const float4*>(p);
         b = *reinterpret_cast<const float4*>(p + 4);
     }
-    __device__ __forceinline__ void zero() { a = b = make_float4(0.0f, 0.0f, 0.0f, 0.0f); }
     __device__ __forceinline__ void get(float (&v)[8]) const {
         v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
     }
     __device__ __forceinline__ uint32_t amax() const {
-        float f[8];
-        get(f);
-        uint32_t m = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) m = max(m, __float_as_uint(f[k]) & 0x7FFFFFFFu);
-        return m;
+        return __float_as_uint(max3(max3(max3(max3(0.0f, a.x, a.y), a.z, a.w), b.x, b.y), b.z, b.w));
     }
 };
 constexpr int STAGE_U = 4;  // chunks of a lane in flight
@@ -272,6 +278,7 @@ constexpr int STAGE_U = 4;  // chunks of a lane in flight
 template <int W>
 __device__ __forceinline__ int warps_per_row(int n) {
     int wpr = W;
+#pragma unroll 1
     while (wpr > 1 && n * wpr > W) wpr >>= 1;
     return wpr;
 }
@@ -286,8 +293,8 @@ template <typename In>
 __device__ __forceinline__ void load_chunks(Chunk<In> (&v)[STAGE_U], const In* row, int q, int step, int chunks) {
 #pragma unroll
     for (int u = 0; u < STAGE_U; ++u) {
-        if (q + u * step < chunks) v[u].load(row + 8 * (q + u * step));
-        else v[u].zero();
+        if (q + u * step >= chunks) break;
+        v[u].load(row + 8 * (q + u * step));
     }
 }
 // Ends with the rows visible to all threads. `loaded`: the caller has made
@@ -301,21 +308,28 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
     const int chunks = K / 8, padded = (chunks + PC - 1) / PC * PC;
     const int q0 = (warp & (wpr - 1)) * 32 + lane, step = 32 * wpr;
     const int lw = 31 - __clz(wpr);
+#pragma unroll 1
     for (int i = threadIdx.x; i < n; i += 32 * W) amax[i] = 0u;
     __syncthreads();
     const bool keep = staged_from_registers<W>(n, K);
+#pragma unroll 1
     for (int i = warp >> lw; i < n; i += W >> lw) {
         const In* row = src(i);
         uint32_t m = 0;
+#pragma unroll 1
         for (int q = q0; q < chunks; q += STAGE_U * step) {
             if (!loaded) load_chunks(v, row, q, step, chunks);
 #pragma unroll
-            for (int u = 0; u < STAGE_U; ++u) m = max(m, v[u].amax());
+            for (int u = 0; u < STAGE_U; ++u) {
+                if (q + u * step >= chunks) break;
+                m = max(m, v[u].amax());
+            }
         }
         m = __reduce_max_sync(0xffffffffu, m);
         if (lane == 0) atomicMax(amax + i, m);
     }
     __syncthreads();
+#pragma unroll 1
     for (int i = warp >> lw; i < n; i += W >> lw) {
         const In* row = src(i);
         const uint32_t m = amax[i];
@@ -326,12 +340,13 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
         const int sa = max(-100, min(100, sh));
         const float fa = pow2(sa), fb = pow2(sh - sa);
         if (q0 == 0) unshift[i] = pow2(-sa) * pow2(sa - sh);
+#pragma unroll 1
         for (int q = q0; q < padded; q += STAGE_U * step) {
             if (!keep) load_chunks(v, row, q, step, chunks);
 #pragma unroll
             for (int u = 0; u < STAGE_U; ++u) {
                 const int c = q + u * step;
-                if (c >= padded) continue;
+                if (c >= padded) break;
                 float f[8];
                 v[u].get(f);
                 uint32_t h[4];
@@ -381,6 +396,7 @@ __device__ __forceinline__ Routing build_routing(const Args& a, uint8_t* mem, in
     const int lane = threadIdx.x % 32;
     // `c` slots of expert e, from entry `first` on: lane by lane one more set of jobs
     auto emit = [&](int e, int c, int first, int at) {
+#pragma unroll 1
         for (int k = 0; k < c; k += columns, ++at) {
             r.expert[at] = e;
             r.start[at] = first + k;
@@ -530,8 +546,12 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     // read before the wait, h not.
     if constexpr (MODE == UP || MODE == DENSE) {
         grid_dependency_wait();
-        grid_launch_dependents();
+        if (MODE == DENSE || WARPS != 8) grid_launch_dependents();
     }
+    // UP beside whose CTAs the next kernel's find room: they start when the
+    // operand is staged, so that their first copies do not hold up this
+    // kernel's, unless there is little to stream after that (us a call, started
+    // at once and late: FP8 1 token 14.0, 13.5; 1024 x 512, top-4 9.9, 10.5).
     // The operand's loads are made early, before the weights fill the memory
     // system's queues: all tokens (by_token) before the routing, else the first
     // group's rows after it.
@@ -574,6 +594,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         int tile, j = tile_job(f, tile);
         const int most = job_start(j) + a.P;
         ++j;
+#pragma unroll 1
         while (j * job_tiles < u0 + share && job_start(j + 1) <= most) ++j;
         return min(j * job_tiles - u0, share);
     };
@@ -606,6 +627,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     const uint8_t *wp0 = nullptr, *wp1 = nullptr, *sp = nullptr;
     auto next_tile = [&](uint32_t place) {
         rf += teams;
+#pragma unroll 1
         while (rf >= rend) {
             if (rend >= total) {
                 rf = rend = total;
@@ -640,36 +662,29 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             cp_async4(place + G::GLOBAL + 4 * lane, a.w.s + e, false);
         }
     };
-    // the piece `off` bytes further on in the rows
-    auto copy_piece = [&](uint32_t to, int off) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const bool past = rrem <= off + 64 * h;
-            cp_async16(to + 1024 * h + 16 * lane, wp0 + off + 64 * h, past);
-            cp_async16(to + 1024 * h + 512 + 16 * lane, wp1 + off + 64 * h, past);
-        }
-        if constexpr (FMT == NVFP4) {
-            const int chunks = off >> 5;  // 32 code bytes each
-            if constexpr (MODE == OWN) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    cp_async4(to + G::WORDS + 128 * h + 4 * lane, sp + 512 * chunks + 1024 * h, srem <= chunks + 2 * h);
-            } else if (lane < 16) {
-                cp_async16(to + G::WORDS + 16 * lane, sp + 512 * chunks, srem <= chunks);
-            }
-        }
-    };
-    auto request = [&](uint32_t place) {
-        if (rleft == 0 && rf < total) next_tile(place);
+    auto request = [&](uint32_t to) {
+        if (rleft == 0 && rf < total) next_tile(to);
         if (rleft > 0) {
-            copy_piece(place, 0);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const bool past = rrem <= 64 * h;
+                cp_async16(to + 1024 * h + 16 * lane, wp0 + 64 * h, past);
+                cp_async16(to + 1024 * h + 512 + 16 * lane, wp1 + 64 * h, past);
+            }
             wp0 += 128 * ks;
             wp1 += 128 * ks;
+            rrem -= 128 * ks;
             if constexpr (FMT == NVFP4) {
+                if constexpr (MODE == OWN) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        cp_async4(to + G::WORDS + 128 * h + 4 * lane, sp + 1024 * h, srem <= 2 * h);
+                } else if (lane < 16) {
+                    cp_async16(to + G::WORDS + 16 * lane, sp, srem <= 0);
+                }
                 sp += 2048 * ks;
                 srem -= 4 * ks;
             }
-            rrem -= 128 * ks;
             --rleft;
         }
         cp_async_commit();
@@ -683,37 +698,24 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             load_early(n, [&](int i) { return in + static_cast<int64_t>(MODE == DENSE ? base + i : rt.row[base + i]) * K; });
         }
     }
-    // fill the ring: the first tile's pieces side by side, then the next tiles'
-    if (rf < total) next_tile(ring);
-    const int ahead = min(rleft, DEPTH);
-#pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-        if (d < ahead) {
-            copy_piece(ring + d * G::SLOT, 128 * ks * d);
-            cp_async_commit();
-        }
-    }
-    wp0 += 128 * ks * ahead;
-    wp1 += 128 * ks * ahead;
-    if constexpr (FMT == NVFP4) {
-        sp += 2048 * ks * ahead;
-        srem -= 4 * ks * ahead;
-    }
-    rrem -= 128 * ks * ahead;
-    rleft -= ahead;
+    const bool late = MODE == UP && WARPS == 8 && 2 * total * kp > WARPS * DEPTH;
+    if (MODE == UP && WARPS == 8 && !late) grid_launch_dependents();
+    // fill the ring
 #pragma unroll 1
-    for (int d = ahead; d < DEPTH; ++d) request(ring + d * G::SLOT);
+    for (int d = 0; d < DEPTH; ++d) request(ring + d * G::SLOT);
     uint32_t place = ring;  // of the oldest piece
 
     // OWN: outputs per slot and row of 16; the slots' routing weights behind them
     float* own = reinterpret_cast<float*>(smem + L.own);
     if constexpr (MODE == OWN) {
+#pragma unroll 1
         for (int s = threadIdx.x; s < a.S; s += THREADS) {
             const int id = a.ids[s];
             own[a.S * 16 + s] = a.tw[s];
             // outputs of a slot without an expert stay zero, and so does its weight
             if (id < 0 || id >= a.E) {
                 own[a.S * 16 + s] = 0.0f;
+#pragma unroll 1
                 for (int i = 0; i < 16; ++i) own[s * 16 + i] = 0.0f;
             }
         }
@@ -736,6 +738,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                 return in + static_cast<int64_t>(by_token ? i : MODE == DENSE ? base + i : rt.row[base + i]) * K;
             });
             loaded = false;
+            if (late && f0 == 0) grid_launch_dependents();
         }
         const int own_row = MODE == OWN ? 16 * (f0 / max(rt.jobs, 1)) : 0;  // of the share
         for (int fr = f0; fr < f1; fr += teams) {
