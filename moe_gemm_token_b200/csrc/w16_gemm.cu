@@ -35,8 +35,8 @@
 // Every mbarrier wait is bounded by the device watchdog.
 //
 // With FP4 the weights are NVFP4 (launch_nvfp4_w4a16_tensor): a converter
-// thread reads 32 code bytes and one word of four block scales per stage, PF
-// = 8 stages ahead, and widens D2(q) D(sf) exactly (FP16 product, six
+// thread reads 32 code bytes and one word of four block scales per stage, two
+// stages ahead, and widens D2(q) D(sf) exactly (FP16 product, six
 // significant bits); the epilogue applies the one global scale. Tiles of 32
 // and 64 tokens keep the MMAs of few tokens short (N = 32 or 64). What bounds
 // a CTA is the issue of the MMAs (8 a stage of 0.55 us, whatever N up to
@@ -52,9 +52,12 @@ constexpr int TILE_N = 128;      // channels per tile (TMEM lanes)
 constexpr int A_COLS = BKE / 2;  // TMEM columns per weight stage (two BF16 per column)
 constexpr int TMEM_COLS = 512;
 constexpr int CONV_WARPS = 8;   // two per TMEM lane quadrant, each on half of a stage
-// stages of weight bytes in flight per converter thread
+// Stages of weight bytes in flight per converter thread. NVFP4 (us, 37 tokens
+// 6144 x 2048, 64 tokens 14336 x 4096): 8 stages 9.9, 23.2; 4 stages 9.2, 22.3;
+// 2 stages 8.8, 22.0; 1 stage 8.6, 27.9. Every load of a warp touches 32 lines,
+// so deeper loads delay the first stages.
 template <bool FP4>
-constexpr int pf() { return FP4 ? 8 : 4; }
+constexpr int pf() { return FP4 ? 2 : 4; }
 constexpr int THREADS = 64 + CONV_WARPS * 32 + 4 * 32;
 
 // Tiles of TM tokens (accumulator columns). TM = 128: two accumulators (the
