@@ -1113,14 +1113,14 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
 
 // metis_nvfp4_w4a16_gemm by its tokens, measured on B200 (us; N x K):
 //                        6144x2048   14336x4096   2048x6144   1024x1024   4096x14336
-//     1  streamed             5.4        11.1         5.1         3.6        12.3
-//        tensor cores         9.2        22.5         9.5         4.3        20.9
-//     8  streamed             7.0        13.9        10.0         4.0        30.7
-//        tensor cores         9.4        22.5         9.6         4.5        21.0
-//    16  streamed             8.8        19.1        13.9         5.1        56.2
-//        tensor cores         9.3        22.2         9.7         4.6        21.2
+//     1  streamed             5.2        10.5         4.9         3.7        12.2
+//        tensor cores         8.2        20.8         8.2         4.1        20.0
+//     8  streamed             6.8        13.7         9.6         4.4        30.9
+//        tensor cores         8.2        20.7         8.3         4.3        20.0
+//    16  streamed             8.3        18.9        13.3         4.9        55.5
+//        tensor cores         8.3        20.8         8.5         4.4        20.2
 //    32  streamed            21.6        52.5
-//        tensor cores         9.8        22.3
+//        tensor cores         8.5        21.0
 //  2048  tensor cores        48.5
 //        widened first       50.7
 //  4096  tensor cores        92.2
@@ -1128,12 +1128,12 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
 constexpr int64_t kStreamTokens = 16, kWidenTokens = 2048;
 
 // Up to kStreamTokens, by estimates fitted to the table, in ns: 3000 + 100 per
-// 1024 staged operand values + the codes at 3.2 TB/s, against 4000 + 600 per
-// stage. The stream's operand has to fit shared memory in one piece.
+// 1024 staged operand values + the codes at 3.2 TB/s + 500 for a second group
+// of columns, against 3750 + 530 per stage. The stream's operand has to fit
+// shared memory in one piece.
 static bool nvfp4_w4a16_streams(int64_t M, int64_t N, int64_t K, const W4a16Plan& plan) {
-    const int64_t staged = (M <= 8 ? M : kStreamTokens) * K;
     return M <= kStreamTokens && (M == 1 || (M <= 8 ? M : 8) * K <= 80 * 1024) &&
-           staged * 100 / 1024 + N * K / 6400 < 1000 + 600 * plan.stages;
+           M * K * 100 / 1024 + N * K / 6400 + (M > 8 ? 500 : 0) < 750 + 530 * plan.stages;
 }
 
 size_t nvfp4_w4a16_workspace(int64_t M, int64_t N, int64_t K) {

@@ -39,7 +39,7 @@
 // stages ahead, and widens D2(q) D(sf) exactly (FP16 product, six
 // significant bits); the epilogue applies the one global scale. Tiles of 32
 // and 64 tokens keep the MMAs of few tokens short (N = 32 or 64). What bounds
-// a CTA is the issue of the MMAs (8 a stage of 0.55 us, whatever N up to
+// a CTA is the issue of the MMAs (8 a stage of 0.5 us, whatever N up to
 // 128), so a tile's K is split over a cluster while SMs are free (SPLIT).
 #include "common.cuh"
 
@@ -586,7 +586,7 @@ int prepare_fp4(const DeviceInfo& di) {
 }  // namespace w16
 
 // The tile width and the split for an NVFP4 weight-only product, and the
-// stages (of 128 elements of K, 0.6 us each) that its CTAs do one after another.
+// stages (of 128 elements of K, 0.5 us each) that its CTAs do one after another.
 int plan_nvfp4_w4a16_tensor(int M, int N, int K, W4a16Plan* plan) {
     using namespace w16;
     DeviceInfo di;
@@ -597,9 +597,10 @@ int plan_nvfp4_w4a16_tensor(int M, int N, int K, W4a16Plan* plan) {
         W4a16Plan w;
         w.tm = tm;
         w.tiles = static_cast<int64_t>((M + tm - 1) / tm) * (N / TILE_N);
-        // CTAs per tile: as many as are resident at once (37 tokens: 6144 x 2048
-        // 13.2 us with one, 9.9 with two; 2048 x 6144 30.6 with one, 10.2 with six;
-        // a second wave of clusters costs more than the split gains: 16.2 with three)
+        // CTAs per tile: as many as are resident at once (37 tokens, with the
+        // deeper loads of that time: 6144 x 2048 13.2 us with one, 9.9 with two; 2048 x
+        // 6144 30.6 with one, 10.2 with six; a second wave of clusters costs more than
+        // the split gains: 16.2 with three)
         w.ks = num_kb < MAX_KS ? num_kb : MAX_KS;
         while (w.ks > 1 && w.tiles > resident[di.device & 63][w.ks].load(std::memory_order_relaxed)) --w.ks;
         w.stages = (w.tiles + di.num_sms - 1) / di.num_sms * ((num_kb + w.ks - 1) / w.ks);
