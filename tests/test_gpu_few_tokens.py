@@ -1,5 +1,9 @@
 """Default maths for few tokens against plain 64-bit forms: the routed layer
 with FP8 and NVFP4 experts, and the NVFP4 weight-only product."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -85,10 +89,12 @@ def check(metis, fmt, d, what=""):
 FP8_SIZES = [(1, 16, 16, 1, 1), (1, 2048, 1024, 64, 8), (3, 80, 48, 5, 2), (8, 272, 144, 8, 8), (9, 1040, 528, 24, 3),
              (17, 256, 512, 4, 4), (64, 512, 256, 16, 4), (128, 128, 128, 8, 8), (2, 8192, 16, 3, 1),
              (2, 16, 8192, 3, 2), (33, 4096, 1040, 6, 2), (5, 8192, 2064, 3, 2), (40, 2048, 1024, 32, 8),
-             (1, 1008, 992, 2, 2), (6, 2048, 1040, 1024, 5)]
+             (1, 1008, 992, 2, 2), (6, 2048, 1040, 1024, 5), (1, 64, 48, 1024, 1024), (1, 128, 112, 65, 65),
+             (1, 128, 112, 64, 64), (16, 80, 32, 64, 64), (4, 8192, 8192, 2, 2), (128, 32, 16, 1, 1)]
 FP4_SIZES = [(1, 128, 128, 1, 1), (1, 2048, 1024, 64, 8), (5, 384, 256, 7, 3), (17, 640, 896, 4, 4),
              (64, 1024, 512, 16, 4), (128, 128, 128, 8, 8), (2, 8192, 128, 2, 2), (2, 128, 8192, 2, 2),
-             (33, 1152, 1664, 6, 2), (40, 2048, 1024, 32, 8), (3, 256, 128, 1024, 7)]
+             (33, 1152, 1664, 6, 2), (40, 2048, 1024, 32, 8), (3, 256, 128, 1024, 7), (1, 128, 256, 1024, 1024),
+             (1, 256, 128, 65, 65), (1, 256, 128, 64, 64), (16, 128, 256, 64, 64), (4, 8192, 8192, 2, 2)]
 
 
 @pytest.mark.parametrize("T,H,I,E,k", FP8_SIZES)
@@ -345,6 +351,51 @@ def test_moe_weights_past_32_bit_offsets(metis, fmt):
     y = run(metis, fmt, big)
     assert metis.metis_check_device_status() == 0
     assert_within(y, *expect(fmt, small))
+
+
+FIRST_CALLS_CAPTURED = """
+import torch
+from moe_gemm_token_b200 import metis
+def u8(*s): return torch.randint(0, 120, s, device="cuda", dtype=torch.uint8)
+T, H, I, E, k, N = 3, 256, 128, 4, 2, 384
+x = torch.randn(2100, H, device="cuda").bfloat16()
+ids = torch.tensor([[0, 1], [2, 3], [1, 1]], dtype=torch.int32, device="cuda")
+tw, g, one = torch.ones(T, k, device="cuda"), torch.full((E,), 1e-3, device="cuda"), torch.ones(1, device="cuda")
+fp8 = (u8(E, I, H), torch.full((E, I), 1e-3, device="cuda"), u8(E, H, I), torch.full((E, H), 1e-3, device="cuda"))
+fp4 = (u8(E, I, H // 2), u8(E * I * H // 16), g, u8(E, H, I // 2), u8(E * H * I // 16), g)
+w, wsf = u8(N, H // 2), u8(N * H // 16)
+ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+q, sf = torch.zeros(128, H // 2, dtype=torch.uint8, device="cuda"), torch.empty(128 * H // 32, dtype=torch.uint8, device="cuda")
+out = [torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+       for m, n in ((T, H), (T, H), (3, N), (40, N), (2100, N), (40, H), (40, 128))]
+metis.load()
+def run():
+    metis.metis_moe_w8a16(x[:T], ids, tw, *fp8, out[0], ws)
+    metis.metis_moe_nvfp4_w4a16(x[:T], ids, tw, *fp4, out[1], ws)
+    for y in out[2:5]:
+        metis.metis_nvfp4_w4a16_gemm(x[:len(y)], w, wsf, one, y, ws)
+    metis.metis_quant_mxfp4(x[:40], q[:40], sf, tiled=True)
+    metis.metis_dequant_mxfp4(q[:40], sf, out[5], tiled=True)
+    metis.metis_mxfp4_gemm(q, sf, q, sf, out[6])
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run()
+for y in out:
+    y.fill_(float("nan"))
+graph.replay()
+torch.cuda.synchronize()
+first = [y.clone() for y in out]
+run()
+assert all(torch.equal(a, b) for a, b in zip(first, out)) and metis.metis_check_device_status() == 0
+"""
+
+
+def test_first_calls_of_a_process_captured_together():
+    """Every operator's first call of a process inside one capture; the replay equals the calls after it."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS_CAPTURED], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr[-2000:]
 
 
 @by_format
