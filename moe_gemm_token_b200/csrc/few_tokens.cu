@@ -548,10 +548,6 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         grid_dependency_wait();
         if (MODE == DENSE || WARPS != 8) grid_launch_dependents();
     }
-    // UP beside whose CTAs the next kernel's find room: they start when the
-    // operand is staged, so that their first copies do not hold up this
-    // kernel's, unless there is little to stream after that (us a call, started
-    // at once and late: FP8 1 token 14.0, 13.5; 1024 x 512, top-4 9.9, 10.5).
     // The operand's loads are made early, before the weights fill the memory
     // system's queues: all tokens (by_token) before the routing, else the first
     // group's rows after it.
@@ -698,6 +694,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             load_early(n, [&](int i) { return in + static_cast<int64_t>(MODE == DENSE ? base + i : rt.row[base + i]) * K; });
         }
     }
+    // UP beside whose CTAs the next kernel's find room: they start when the
+    // operand is staged, so that their first copies do not hold up this
+    // kernel's, unless there is little to stream after that (us a call, started
+    // at once and late: FP8 1 token 14.0, 13.5; 1024 x 512, top-4 9.9, 10.5).
     const bool late = MODE == UP && WARPS == 8 && 2 * total * kp > WARPS * DEPTH;
     if (MODE == UP && WARPS == 8 && !late) grid_launch_dependents();
     // fill the ring
