@@ -184,7 +184,7 @@ METIS_API int metis_moe_nvfp4_w4a16(const void* x_bf16, const int32_t* topk_ids,
  * (x keeps its BF16 values, elements below 2^-29 of a token's largest
  * magnitude lose bits); otherwise they are multiplied as BF16.
  *   workspace  metis_workspace_size(METIS_OP_NVFP4_W4A16, M, N, K, 0, 0)
- *              bytes, 256-byte aligned: 0 (NULL allowed) up to 2048 tokens;
+ *              bytes, 256-byte aligned: 0 (NULL allowed) up to 3000 tokens;
  *              beyond, the widened weights. Overwritten: calls that may
  *              overlap on the GPU need one each.
  */

@@ -1121,11 +1121,13 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
 //        tensor cores         8.3        20.8         8.5         4.4        20.2
 //    32  streamed            21.6        52.5
 //        tensor cores         8.5        21.0
-//  2048  tensor cores        48.5
-//        widened first       50.7
-//  4096  tensor cores        92.2
-//        widened first       82.4
-constexpr int64_t kStreamTokens = 16, kWidenTokens = 2048;
+//  2048  tensor cores        44.0       178          39.2         9.3
+//        widened first       50.1       199          51.7        13.3
+//  3000  tensor cores        61.1                    67 - 72     12.3
+//        widened first       63.0                    79 - 85     14.8
+//  4096  tensor cores        90.9                    80          14.2
+//        widened first       82.5                    84          17.8
+constexpr int64_t kStreamTokens = 16, kWidenTokens = 3000;
 
 // Up to kStreamTokens, by estimates fitted to the table, in ns: 3000 + 100 per
 // 1024 staged operand values + the codes at 3.2 TB/s + 500 for a second group

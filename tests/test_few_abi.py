@@ -85,11 +85,11 @@ def test_nvfp4_product_refuses(lib):
     assert call(gb=P + 2) == BAD
     assert call(M=0, x=None, y=None) == OK
     op = metis.METIS_OP_NVFP4_W4A16
-    assert metis.metis_workspace_size(op, 2048, 256, 128) == 0
-    need = metis.metis_workspace_size(op, 2049, 256, 128)
+    assert metis.metis_workspace_size(op, 3000, 256, 128) == 0
+    need = metis.metis_workspace_size(op, 3001, 256, 128)
     assert need == 2 * 256 * 128 + 4 * 256
     for ws, size in ((None, BIG), (P, need - 1), (P + 16, need)):
-        assert call(M=2049, ws=ws, size=size) == BAD and str(need) in message(lib)
+        assert call(M=3001, ws=ws, size=size) == BAD and str(need) in message(lib)
 
 
 def test_mxfp4_quantizer_refuses(lib):
