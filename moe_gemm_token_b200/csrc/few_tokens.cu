@@ -297,20 +297,24 @@ __device__ __forceinline__ void load_chunks(Chunk<In> (&v)[STAGE_U], const In* r
         v[u].load(row + 8 * (q + u * step));
     }
 }
-// Ends with the rows visible to all threads. `loaded`: the caller has made
-// the loads (staged_from_registers holds); `maxima`: and found each warp's
-// largest magnitude, [n][W].
-template <int FMT, int W, typename In, typename Src>
+// Ends with the rows visible to all threads. WHOLE: nothing is loaded before,
+// and a warp takes whole rows when its registers hold one, both steps of a row
+// after one read of it (us a call: 5 tokens, odd, 14.3 -> 13.0, 2 tokens 20.2 ->
+// 18.6, 1 token 12.8 -> 12.5). `loaded`: the caller has made the loads
+// (staged_from_registers holds); `maxima`: and found each warp's largest
+// magnitude, [n][W].
+template <int FMT, int W, bool WHOLE, typename In, typename Src>
 __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch, float* unshift, uint32_t* amax,
                                            Chunk<In> (&v)[STAGE_U], bool loaded, const uint32_t* maxima, Src&& src) {
     constexpr int PC = Geo<FMT>::EL / 4;  // chunks of a piece
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int wpr = warps_per_row<W>(n);
+    const bool whole = WHOLE && K / 8 <= 32 * STAGE_U;
+    const int wpr = whole ? 1 : warps_per_row<W>(n);
     const int chunks = K / 8, padded = (chunks + PC - 1) / PC * PC;
     const int q0 = (warp & (wpr - 1)) * 32 + lane, step = 32 * wpr;
     const int lw = 31 - __clz(wpr);
     const bool keep = staged_from_registers<W>(n, K);
-    if (!maxima) {
+    if (!maxima && !whole) {
 #pragma unroll 1
         for (int i = threadIdx.x; i < n; i += 32 * W) amax[i] = 0u;
         __syncthreads();
@@ -335,7 +339,19 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
 #pragma unroll 1
     for (int i = warp >> lw; i < n; i += W >> lw) {
         const In* row = src(i);
-        const uint32_t m = maxima ? __reduce_max_sync(0xffffffffu, lane < wpr ? maxima[i * W + lane] : 0u) : amax[i];
+        uint32_t m;
+        if (whole) {
+            load_chunks(v, row, q0, step, chunks);
+            m = 0;
+#pragma unroll
+            for (int u = 0; u < STAGE_U; ++u) {
+                if (q0 + u * step >= chunks) break;
+                m = max(m, v[u].amax());
+            }
+        } else {
+            m = maxima ? (lane < wpr ? maxima[i * W + lane] : 0u) : amax[i];
+        }
+        m = __reduce_max_sync(0xffffffffu, m);
         // floor(log2(m)) = bits' exponent - 127; a subnormal m has its leading bit at 31 - clz
         const int lg = m >= 0x00800000u ? static_cast<int>(m >> 23) - 127 : 31 - __clz(m) - 149;
         const int sh = m == 0 || m >= 0x7F800000u ? 0 : 14 - lg;
@@ -345,7 +361,7 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
         if (q0 == 0) unshift[i] = pow2(-sa) * pow2(sa - sh);
 #pragma unroll 1
         for (int q = q0; q < padded; q += STAGE_U * step) {
-            if (!keep) load_chunks(v, row, q, step, chunks);
+            if (!keep && !whole) load_chunks(v, row, q, step, chunks);
 #pragma unroll
             for (int u = 0; u < STAGE_U; ++u) {
                 const int c = q + u * step;
@@ -760,7 +776,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         if (!(MODE == OWN || by_token) || f0 == 0) {
             if (f0 > 0) __syncthreads();
             const int n = by_token ? a.T : job_start(MODE == OWN ? rt.jobs : tile_job(f1 - 1, unused) + 1) - base;
-            stage_rows<FMT, WARPS, In>(n, K, xs, a.pitch, unshift, amax, early, loaded, maxima, [&](int i) {
+            stage_rows<FMT, WARPS, MODE == DOWN || MODE == OWN, In>(n, K, xs, a.pitch, unshift, amax, early, loaded, maxima, [&](int i) {
                 return in + static_cast<int64_t>(by_token ? i : MODE == DENSE ? base + i : rt.row[base + i]) * K;
             });
             loaded = false;
