@@ -251,8 +251,8 @@ METIS_API int metis_moe_fp8_grouped_gemm_noalloc(const void* x_bf16, const int32
  *   y[t]    = bf16_rn( sum_j topk_w[t, j] o[t, j] ),
  * products of 16-bit values with FP32 sums. x keeps its BF16 values (elements
  * below 2^-29 of the token's largest magnitude lose bits, and below 2^-39 of
- * it count as zero); h is held in FP32 and rounded to 11 significant bits
- * (FP16 after a power-of-two shift of its row) where it is multiplied.
+ * it count as zero); h is held in FP32 and multiplied as the sum of two FP16
+ * values (off by at most 2^-22 of each element, or 2^-39 of its row's largest).
  *   x [T, H] BF16, topk_ids [T, topk] int32 in [0, E), topk_w [T, topk] FP32,
  *   w_up [E, I, H] E4M3, s_up [E, I], w_down [E, H, I] E4M3, s_down [E, H],
  *   y [T, H] BF16 out. act must be METIS_ACT_NONE.

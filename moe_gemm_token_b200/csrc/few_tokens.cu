@@ -21,8 +21,11 @@
 //    there are fewer tiles than warps; their sums meet in shared memory.
 //  * The operand (x, then h) is staged as FP16 after a power-of-two shift of
 //    its row: BF16 values keep all their bits within 2^-29 of the row's
-//    largest, FP32 values are rounded to 11 bits (a quarter of what rounding
-//    h to BF16 would cost in the result; the sums stay FP32).
+//    largest. FP32 values become two FP16 values, the rounded one and the
+//    rounded rest (22 significant bits, 2^-39 of the row's largest): two
+//    columns of the MMA whose sums are added. One FP16 value alone would put
+//    0.0009 (RMS) between the results and those of FP32 sums; two keep what
+//    the FP32 sums give, and cost no MMA while a job has up to 4 slots.
 //  * Few slots (h of all of them fits a CTA): the down-projection's CTAs own
 //    output rows for every job and finish y themselves, two launches in all
 //    (OWN). More: o goes through the workspace and combine_kernel (DOWN).
@@ -60,18 +63,24 @@ struct Weights {
 
 enum Mode { UP = 0, DOWN = 1, OWN = 2, DENSE = 3 };
 
+// FP16 values that an operand element is staged as, each a row of its own.
+template <int MODE>
+constexpr int PARTS = MODE == DOWN || MODE == OWN ? 2 : 1;
+
 // Geometry by warps per CTA: 8 warps leave room on an SM for a CTA of the next
 // kernel, whose prologue then overlaps (few weights per SM: latency); 16 take
 // an SM by themselves and share one staged operand (many weights per SM).
 // DEPTH: pieces (2 KB) in flight per warp. 8 warps: OWN shares the SM with the
-// up-projection and reads its pieces ahead while that one runs (FP8, 1 token,
-// UP 4 and OWN 5 pieces 12.95 us a call, 3 and 5 13.1, 3 and 6 13.4, 2 and 5
-// 14.2; NVFP4 3 pieces 12.07, 4 pieces 12.17, 5 pieces 14.6). 16 warps, us per
+// up-projection, where both fit, and reads its pieces ahead while that one runs
+// (us a call, OWN with 3, 4 and 5 pieces: FP8 1 token 2048 x 1024 13.1, 12.7,
+// 12.6; 4 tokens top-4 2048 x 512 13.9, 13.5, 15.9, where 5 do not fit; 1 token
+// 4096 x 1024 21.4, 19.4, 19.3; NVFP4 1 token 3 pieces 12.07, 4 pieces 12.17, 5
+// pieces 14.6). 16 warps, us per
 // call: FP8, 32 tokens 2 pieces 57.0, 3 pieces 56.4; NVFP4, which its
 // widening instructions bound, 64 tokens 2 pieces 28.3, 3 pieces 29.2.
 template <int FMT, int MODE, int GMAX, int W>
 struct Cta {
-    static constexpr int DEPTH = W == 8     ? (FMT == NVFP4 ? 3 : MODE == OWN ? 5 : 4)
+    static constexpr int DEPTH = W == 8     ? (FMT == NVFP4 ? 3 : 4)
                                  : FMT == FP8 ? 3
                                               : 2;
 };
@@ -100,7 +109,7 @@ struct Args {
     int P;                 // operand rows that are staged at a time, at most
     int by_token;          // UP: all tokens are staged, before the routing is known
     uint32_t grid_inv, tiles_inv;  // floor((2^32 - 1) / d) of the grid and of the tiles of a job
-    int pitch;             // bytes between staged rows: 64 mod 128
+    int pitch;             // bytes between staged FP16 rows: 64 mod 128
     void* out;             // UP, DOWN: FP32 [S, N]; OWN: BF16 [T, N]; DENSE: BF16 [T, N]
     uint32_t* status;
 };
@@ -136,7 +145,7 @@ __host__ __device__ inline Smem smem_layout(int slot_bytes, int P, int pitch, in
     Smem s;
     s.part = W * Cta<FMT, MODE, GMAX, W>::DEPTH * slot_bytes;
     s.x = s.part + (GMAX == 1 ? 2 : 1) * W * 512 * GMAX;
-    s.unshift = s.x + P * pitch;
+    s.unshift = s.x + P * PARTS<MODE> * pitch;
     s.items = s.unshift + ((P * 8 + 15) & ~15);
     s.route = s.items + 2 * W * static_cast<int>(sizeof(Item));
     s.own = s.route + (routed ? 4 * (E + 4 * S + 18) : 16);
@@ -218,18 +227,19 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 
 // Operand rows [K] are staged as FP16 after the power-of-two shift that
 // brings a row's largest magnitude into [2^14, 2^15) (exact for BF16 values
-// within 2^-29 of the largest; FP32 values are rounded to 11 significant
-// bits). A row with an infinity or a NaN is not shifted. 16-byte chunks are
-// stored in the order in which the lanes read them (operand_chunk), zeros
-// from K to the end of the last piece.
+// within 2^-29 of the largest; FP32 values with PARTS = 2 lose less than 2^-22
+// of theirs or 2^-39 of the largest). A row with an infinity or a NaN is not
+// shifted, and its second parts are zeros. 16-byte chunks are stored in the
+// order in which the lanes read them (operand_chunk), zeros from K to the end
+// of the last piece.
 template <int FMT>
 __device__ __forceinline__ int operand_chunk(int q) {
     constexpr int C = Geo<FMT>::CH;  // a half's chunk t * C + i is stored at i * 4 + t
     const int piece = q / (4 * C), r = q % (4 * C);
     return piece * 4 * C + (r % C) * 4 + r / C;
 }
-// Staging n operand rows by all warps: row i is src(i) and goes to dst + i *
-// pitch. W / n' warps share a row (n' = n rounded up to a power of two), so
+// Staging n operand rows by all warps: row i is src(i) and its part j goes to
+// dst + (PARTS * i + j) * pitch. W / n' warps share a row (n' = n rounded up to a power of two), so
 // that a few rows are read with one round trip, and a lane keeps its chunks
 // in registers between the two steps (largest magnitude, shift) when they fit.
 // The largest magnitude of three, NaN if one of them is NaN.
@@ -303,7 +313,7 @@ __device__ __forceinline__ void load_chunks(Chunk<In> (&v)[STAGE_U], const In* r
 // 18.6, 1 token 12.8 -> 12.5). `loaded`: the caller has made the loads
 // (staged_from_registers holds); `maxima`: and found each warp's largest
 // magnitude, [n][W].
-template <int FMT, int W, bool WHOLE, typename In, typename Src>
+template <int FMT, int W, int PARTS, bool WHOLE, typename In, typename Src>
 __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch, float* unshift, uint32_t* amax,
                                            Chunk<In> (&v)[STAGE_U], bool loaded, const uint32_t* maxima, Src&& src) {
     constexpr int PC = Geo<FMT>::EL / 4;  // chunks of a piece
@@ -354,7 +364,8 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
         m = __reduce_max_sync(0xffffffffu, m);
         // floor(log2(m)) = bits' exponent - 127; a subnormal m has its leading bit at 31 - clz
         const int lg = m >= 0x00800000u ? static_cast<int>(m >> 23) - 127 : 31 - __clz(m) - 149;
-        const int sh = m == 0 || m >= 0x7F800000u ? 0 : 14 - lg;
+        const bool finite = m < 0x7F800000u;
+        const int sh = m == 0 || !finite ? 0 : 14 - lg;
         // 2^sh and 2^-sh may leave FP32's normal range: two factors
         const int sa = max(-100, min(100, sh));
         const float fa = pow2(sa), fb = pow2(sh - sa);
@@ -368,19 +379,28 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
                 if (c >= padded) break;
                 float f[8];
                 v[u].get(f);
-                uint32_t h[4];
                 if (sa != sh) {
 #pragma unroll
                     for (int k = 0; k < 8; ++k) f[k] *= fb;
                 }
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const __half2 p = __floats2half2_rn(f[2 * k] * fa, f[2 * k + 1] * fa);
-                    h[k] = *reinterpret_cast<const uint32_t*>(&p);
+                for (int j = 0; j < PARTS; ++j) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float lo = j ? f[2 * k] : f[2 * k] * fa, hi = j ? f[2 * k + 1] : f[2 * k + 1] * fa;
+                        const __half2 p = __floats2half2_rn(lo, hi);
+                        h[k] = *reinterpret_cast<const uint32_t*>(&p);
+                        if (j + 1 < PARTS) {  // what the rounding left, exactly
+                            const float2 r = __half22float2(p);
+                            f[2 * k] = finite ? lo - r.x : 0.0f;
+                            f[2 * k + 1] = finite ? hi - r.y : 0.0f;
+                        }
+                    }
+                    // past K: zeros (a second batch there is not what the lane kept)
+                    *reinterpret_cast<uint4*>(dst + (PARTS * i + j) * pitch + 16 * operand_chunk<FMT>(c)) =
+                        c < chunks ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(0, 0, 0, 0);
                 }
-                // past K: zeros (a second batch there is not what the lane kept)
-                *reinterpret_cast<uint4*>(dst + i * pitch + 16 * operand_chunk<FMT>(c)) =
-                    c < chunks ? make_uint4(h[0], h[1], h[2], h[3]) : make_uint4(0, 0, 0, 0);
             }
         }
     }
@@ -546,6 +566,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
     using G = Geo<FMT>;
     constexpr int THREADS = WARPS * 32, DEPTH = Cta<FMT, MODE, GMAX, WARPS>::DEPTH;
     constexpr int LOG = WARPS == 8 ? 3 : 4;
+    // groups of 8 MMA columns in a pass, slots per group, and sums per lane and group
+    constexpr int PT = PARTS<MODE>, GROUPS = GMAX * PT, SLOTS = 8 / PT, SUMS = 4 / PT;
     using In = typename std::conditional<MODE == UP || MODE == DENSE, __nv_bfloat16, float>::type;
     extern __shared__ __align__(128) uint8_t smem[];
     const Smem L = smem_layout<FMT, MODE, GMAX, WARPS>(G::SLOT, a.P, a.pitch, a.E, a.S);
@@ -776,7 +798,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         if (!(MODE == OWN || by_token) || f0 == 0) {
             if (f0 > 0) __syncthreads();
             const int n = by_token ? a.T : job_start(MODE == OWN ? rt.jobs : tile_job(f1 - 1, unused) + 1) - base;
-            stage_rows<FMT, WARPS, MODE == DOWN || MODE == OWN, In>(n, K, xs, a.pitch, unshift, amax, early, loaded, maxima, [&](int i) {
+            stage_rows<FMT, WARPS, PT, MODE == DOWN || MODE == OWN, In>(n, K, xs, a.pitch, unshift, amax, early, loaded, maxima, [&](int i) {
                 return in + static_cast<int64_t>(by_token ? i : MODE == DENSE ? base + i : rt.row[base + i]) * K;
             });
             loaded = false;
@@ -785,11 +807,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
         const int own_row = MODE == OWN ? 16 * (f0 / max(rt.jobs, 1)) : 0;  // of the share
         for (int fr = f0; fr < f1; fr += teams) {
             const bool mine = fr + team < f1;
-            // one group of columns: two chains of MMAs, added at the end
-            constexpr int CHAINS = GMAX == 1 ? 2 : 1;
-            float acc[GMAX * CHAINS][4];
+            // one group of columns (GMAX = 1): two chains of MMAs, added at the end
+            constexpr int ACCS = GROUPS == 1 ? 2 : GROUPS;
+            float acc[ACCS][4];
 #pragma unroll
-            for (int q = 0; q < GMAX * CHAINS; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
+            for (int q = 0; q < ACCS; ++q) acc[q][0] = acc[q][1] = acc[q][2] = acc[q][3] = 0.0f;
             int start = 0, n = 0, p0 = u0 + own_row;
             const int pe = MODE == OWN ? u0 + share : N;
             if (mine) {
@@ -798,15 +820,16 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                 if (MODE != OWN) p0 = 16 * tile;
                 start = job_start(j);
                 n = job_start(j + 1) - start;
-                // columns past n repeat the first one: their sums are not stored
+                // staged row of the job's slot c; slots past n repeat the first one: their
+                // sums are not stored. MMA column g of group q is part g % PT of slot SLOTS q + g / PT.
                 auto column = [&](int c) {
                     const int at = start + (c < n ? c : 0);
                     return by_token ? rt.row[at] : at - base;
                 };
-                uint32_t xp[GMAX];
+                uint32_t xp[GROUPS];
 #pragma unroll
-                for (int q = 0; q < GMAX; ++q)
-                    xp[q] = smem_u32(xs) + column(8 * q + g) * a.pitch + kslice * (4 * G::EL) + 16 * t;
+                for (int q = 0; q < GROUPS; ++q)
+                    xp[q] = smem_u32(xs) + (column(SLOTS * q + g / PT) * PT + g % PT) * a.pitch + kslice * (4 * G::EL) + 16 * t;
                 float sr[2] = {0.0f, 0.0f};
                 if (pieces > 0) {
                     cp_async_wait_oldest<DEPTH>();
@@ -814,7 +837,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                     sr[1] = FMT == FP8 ? __uint_as_float(ld_shared4(place + G::WORDS + 128 + 4 * lane)) : sr[0];
                 }
                 auto run = [&](auto groups) {
-                    constexpr int NG = decltype(groups)::value;
+                    constexpr int NG = decltype(groups)::value, SECOND = GMAX == 1 && NG == 1 ? 1 : 0;
 #pragma unroll 1
                     for (int i = 0; i < pieces; ++i) {
                         cp_async_wait_oldest<DEPTH>();
@@ -857,7 +880,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                                 for (int q = 0; q < NG; ++q) {
                                     const uint4 xv = ld_shared16(xp[q] + 2 * G::EL * h + 64 * c);
                                     mma_16816(acc[q], A[0][0], A[0][1], A[0][2], A[0][3], xv.x, xv.y);
-                                    mma_16816(acc[GMAX * (CHAINS - 1) + q], A[1][0], A[1][1], A[1][2], A[1][3], xv.z, xv.w);
+                                    mma_16816(acc[SECOND + q], A[1][0], A[1][1], A[1][2], A[1][3], xv.z, xv.w);
                                 }
                             }
                         }
@@ -867,23 +890,29 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                         request(place);
                         place = place == ring + (DEPTH - 1) * G::SLOT ? ring : place + G::SLOT;
                     }
-                };
-                if (GMAX == 1 || n <= 8) run(std::integral_constant<int, 1>());
-                else run(std::integral_constant<int, GMAX>());
-                if constexpr (CHAINS == 2) {
+                    if constexpr (SECOND) {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) acc[0][j] += acc[1][j];
-                }
-                // scales: of the rows, and of the columns' operand rows
-#pragma unroll
-                for (int q = 0; q < GMAX; ++q)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float u = unshift[column(8 * q + 2 * t + j)];
-                        acc[q][j] = acc[q][j] * u * sr[0];
-                        acc[q][2 + j] = acc[q][2 + j] * u * sr[1];
+                        for (int j = 0; j < 4; ++j) acc[0][j] += acc[1][j], acc[1][j] = 0.0f;
                     }
+                };
+                constexpr int LESS = GROUPS > 1 ? GROUPS / 2 : 1;  // groups of a job with few slots
+                if (GROUPS == 1 || n <= LESS * SLOTS) run(std::integral_constant<int, LESS>());
+                else run(std::integral_constant<int, GROUPS>());
+                // the parts' sums, then the scales: of the rows, and of the columns' operand rows
+#pragma unroll
+                for (int q = 0; q < GROUPS; ++q) {
+                    if constexpr (PT == 2) acc[q][0] += acc[q][1], acc[q][1] = acc[q][2] + acc[q][3];
+#pragma unroll
+                    for (int j = 0; j < SUMS / 2; ++j) {
+                        const float u = unshift[column(SLOTS * q + SUMS / 2 * t + j)];
+                        acc[q][j] = acc[q][j] * u * sr[0];
+                        acc[q][SUMS / 2 + j] = acc[q][SUMS / 2 + j] * u * sr[1];
+                    }
+                }
             }
+            // slot and place of sum j of a lane (g, t) and group q: SUMS / 2 slots of row g, then of row g + 8
+            auto slot_of = [](int q, int t, int j) { return SLOTS * q + SUMS / 2 * t + j % (SUMS / 2); };
+            auto place_of = [](int p, int g, int j) { return p + g + 8 * (j / (SUMS / 2)); };
             // value v of column c of the job whose slots start at `at`, at place p
             auto put = [&](int at, int c, int p, float v) {
                 const int row = place_to_row<FMT>(p);
@@ -898,10 +927,10 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
             if (ks == 1) {
                 if (mine) {
 #pragma unroll
-                    for (int q = 0; q < GMAX; ++q)
+                    for (int q = 0; q < GROUPS; ++q)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int c = 8 * q + 2 * t + (j & 1), p = p0 + g + 8 * (j >> 1);
+                        for (int j = 0; j < SUMS; ++j) {
+                            const int c = slot_of(q, t, j), p = place_of(p0, g, j);
                             if (c < n && p < pe) put(start, c, p, acc[q][j]);
                         }
                 }
@@ -910,20 +939,22 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                 float* part = reinterpret_cast<float*>(smem + L.part) + buf * (WARPS * 128 * GMAX);
                 if (mine) {
 #pragma unroll
-                    for (int q = 0; q < GMAX; ++q)
-                        if (8 * q < n)
-                            *reinterpret_cast<float4*>(part + (warp * GMAX + q) * 128 + 4 * lane) =
-                                make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
+                    for (int q = 0; q < GROUPS; ++q)
+                        if (SLOTS * q < n) {
+                            float* to = part + (warp * GROUPS + q) * (32 * SUMS) + SUMS * lane;
+                            if constexpr (PT == 2) *reinterpret_cast<float2*>(to) = make_float2(acc[q][0], acc[q][1]);
+                            else *reinterpret_cast<float4*>(to) = make_float4(acc[q][0], acc[q][1], acc[q][2], acc[q][3]);
+                        }
                 }
                 if (kslice == 0 && lane == 0) items[buf * WARPS + team] = Item{start, mine ? n : 0, p0, pe};
                 __syncthreads();
                 for (int o = threadIdx.x; o < teams * GMAX * 128; o += THREADS) {
-                    const int tm = o / (GMAX * 128), q = (o >> 7) % GMAX, at = o & 127;
+                    const int tm = o / (GMAX * 128), q = o / (32 * SUMS) % GROUPS, at = o % (32 * SUMS);
                     const Item it = items[buf * WARPS + tm];
-                    const int c = 8 * q + 2 * ((at >> 2) & 3) + (at & 1), p = it.p + (at >> 4) + 8 * ((at >> 1) & 1);
+                    const int l = at / SUMS, c = slot_of(q, l & 3, at % SUMS), p = place_of(it.p, l >> 2, at % SUMS);
                     if (c >= it.n || p >= it.pe) continue;
                     float sum = 0.0f;
-                    for (int w = 0; w < ks; ++w) sum += part[((tm * ks + w) * GMAX + q) * 128 + at];
+                    for (int w = 0; w < ks; ++w) sum += part[((tm * ks + w) * GROUPS + q) * (32 * SUMS) + at];
                     put(it.slot0, c, p, sum);
                 }
                 if constexpr (GMAX == 1) buf ^= 1;
@@ -1086,15 +1117,16 @@ int launch_few(const DeviceInfo& di, Args a, cudaStream_t st) {
     a.pitch = operand_pitch<FMT>(a.w.K);
     auto bytes = [&](int P) { return smem_layout<FMT, MODE, GMAX, W>(G::SLOT, P, a.pitch, a.E, a.S).total; };
     const int base = bytes(0) + 32;  // rounding
-    const int half = (112 * 1024 - base) / (a.pitch + 8), full = (di.max_smem_optin - base) / (a.pitch + 8);
+    const int row = PARTS<MODE> * a.pitch + 8;
+    const int half = (112 * 1024 - base) / row, full = (di.max_smem_optin - base) / row;
     const int per_job = a.T < 8 * GMAX ? a.T : 8 * GMAX;
-    const int want = MODE == OWN || a.S < 2 * per_job ? a.S : 2 * per_job;
+    // a few tokens that all threads read with one round trip
+    a.by_token = MODE == UP && a.T <= W && static_cast<int64_t>(a.T) * a.w.K <= 8 * STAGE_U * 32 * W;
+    const int want = a.by_token ? a.T : MODE == OWN || a.S < 2 * per_job ? a.S : 2 * per_job;
     const int room = W == 8 && half >= (MODE == OWN ? want : per_job) ? half : full;
     a.P = want < room ? want : room;
-    if (a.P < 1 || (MODE == OWN && a.P < want))
+    if (a.P < 1 || ((MODE == OWN || a.by_token) && a.P < want))
         return fail(METIS_ERR_UNSUPPORTED, "few-token kernel: K=%d is too long", a.w.K);
-    // a few tokens that all threads read with one round trip
-    a.by_token = MODE == UP && a.T <= a.P && a.T <= W && static_cast<int64_t>(a.T) * a.w.K <= 8 * STAGE_U * 32 * W;
     a.grid_inv = 0xFFFFFFFFu / static_cast<uint32_t>(di.num_sms);
     a.tiles_inv = 0xFFFFFFFFu / static_cast<uint32_t>((a.w.N + 15) / 16);
     return cuda_check(launch_pdl(few_kernel<FMT, MODE, GMAX, W>, dim3(di.num_sms), dim3(W * 32), bytes(a.P), st, 1, a),
@@ -1103,11 +1135,14 @@ int launch_few(const DeviceInfo& di, Args a, cudaStream_t st) {
 
 // By the columns that one pass multiplies (8 or 16), the weight bytes that
 // an SM reads (8 against 16 warps, us per call: FP8, 113 KB a projection and SM
-// 17.1, 17.7; NVFP4, 225 KB 42.5, 32.9), and what fits beside long rows.
+// 17.1, 17.7; NVFP4, 225 KB 42.5, 32.9), and what fits beside long rows: 8
+// rows of an operand in one part, 6 (FP8) or 8 (NVFP4) in two (20 tokens top-4
+// on 16 experts 1024 x 4096, the down-projection with 8 and 16 warps: FP8 48.9,
+// 41.6; NVFP4 44.3, 39.9).
 template <int FMT, int MODE>
 int launch_few_by_size(const DeviceInfo& di, const Args& a, int columns, int64_t weight_bytes, cudaStream_t st) {
     const bool small = weight_bytes < di.num_sms * 160ll * 1024;
-    const bool long_rows = operand_pitch<FMT>(a.w.K) * 8 > 112 * 1024;
+    const bool long_rows = PARTS<MODE> * operand_pitch<FMT>(a.w.K) * 8 > (PARTS<MODE> == 2 ? 140 : 112) * 1024;
     if ((columns <= 8 && small) || long_rows) return launch_few<FMT, MODE, 1, 8>(di, a, st);
     if (columns <= 8) return launch_few<FMT, MODE, 1, 16>(di, a, st);
     return launch_few<FMT, MODE, 2, 16>(di, a, st);
@@ -1131,21 +1166,31 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
     a.T = T;
     a.topk = topk;
     a.out = h;
-    // one pass for 16 columns of an expert when their mean calls for it (us a
-    // call on 64 experts, top-8, 2048 x 1024; 8 against 16 columns): FP8 mean 4:
-    // 57.0, 61.8; 8: 65.6, 74.3; 16: 102, 88.8; NVFP4 mean 4: 46.8, 49.2; 8: 64.3, 60.6
+    // one pass for 16 slots of an expert when their mean calls for it (us a call
+    // on 64 experts, top-8, 2048 x 1024; 8 against 16 slots in both projections,
+    // h in one part): FP8 mean 4: 57.0, 61.8; 8: 65.6, 74.3; 16: 102, 88.8; NVFP4
+    // mean 4: 46.8, 49.2; 8: 64.3, 60.6. The down-projection with h in two parts
+    // (8, 16): FP8 mean 12: 81.0, 83.7; 16: 98.0, 101.6, but 24.0, 20.8 on 16
+    // experts 1024 x 512; NVFP4 mean 8: 60.6, 64.5; 12: 77.3, 77.5; 16 on 16
+    // experts 24.2, 21.6; 32: 46.9, 37.5.
     const int columns = S <= (FMT == FP8 ? 10 : 6) * E ? 8 : 16;
     const int64_t weight_bytes = static_cast<int64_t>(S < E ? S : E) * up.N * up.K / (FMT == FP8 ? 1 : 2);
     if ((rc = launch_few_by_size<FMT, UP>(di, a, columns, weight_bytes, st))) return rc;
     a.in = h;
     a.w = down;
-    // few slots: every CTA stages all of h (beside the ring) and owns rows of the output
-    if (S <= 64 && S * operand_pitch<FMT>(down.K) <= 40 * 1024) {
+    // few slots: every CTA stages all of h and owns rows of the output, which
+    // saves the last launch; against DOWN, us a call: 8 slots 2048 x 1024 12.6,
+    // 14.2; 8 slots 512 x 256 7.7, 8.5. With more slots only where the CTA's rows
+    // nearly fill its tiles of 16: 16 slots 2048 x 1024 19.2, 20.0, but 16 slots
+    // 1024 x 512 11.0, 10.5; 24 slots 15.3, 12.2.
+    const int rows = (down.N + di.num_sms - 1) / di.num_sms;
+    const bool filled = 5 * rows >= 4 * 16 * ((rows + 15) / 16);
+    if ((S <= 8 || (S <= 16 && filled)) && PARTS<OWN> * S * operand_pitch<FMT>(down.K) <= 80 * 1024) {
         a.out = y;
         return launch_few<FMT, OWN, 1, 8>(di, a, st);
     }
     a.out = o;
-    if ((rc = launch_few_by_size<FMT, DOWN>(di, a, columns, weight_bytes, st))) return rc;
+    if ((rc = launch_few_by_size<FMT, DOWN>(di, a, S <= 10 * E ? 8 : 16, weight_bytes, st))) return rc;
     return cuda_check(launch_pdl(combine_kernel, dim3((down.N + 511) / 512, T), dim3(128), 0, st, 1,
                                  static_cast<const float*>(o), ids, tw, topk, E, down.N, y),
                       "few-token combine launch");
