@@ -228,10 +228,11 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 // Operand rows [K] are staged as FP16 after the power-of-two shift that
 // brings a row's largest magnitude into [2^14, 2^15) (exact for BF16 values
 // within 2^-29 of the largest; FP32 values with PARTS = 2 lose less than 2^-22
-// of theirs or 2^-39 of the largest). A row with an infinity or a NaN is not
-// shifted, and its second parts are zeros. 16-byte chunks are stored in the
-// order in which the lanes read them (operand_chunk), zeros from K to the end
-// of the last piece.
+// of theirs or 2^-39 of the largest). A row with an infinity or a NaN is
+// shifted as if its largest were 2^128, so that its finite values stay finite
+// (what they add to a sum with an infinity does not matter), and its second
+// parts are zeros. 16-byte chunks are stored in the order in which the lanes
+// read them (operand_chunk), zeros from K to the end of the last piece.
 template <int FMT>
 __device__ __forceinline__ int operand_chunk(int q) {
     constexpr int C = Geo<FMT>::CH;  // a half's chunk t * C + i is stored at i * 4 + t
@@ -362,10 +363,10 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
             m = maxima ? (lane < wpr ? maxima[i * W + lane] : 0u) : amax[i];
         }
         m = __reduce_max_sync(0xffffffffu, m);
-        // floor(log2(m)) = bits' exponent - 127; a subnormal m has its leading bit at 31 - clz
+        // floor(log2(m)) = bits' exponent - 127 (not finite: 128); a subnormal m has its leading bit at 31 - clz
         const int lg = m >= 0x00800000u ? static_cast<int>(m >> 23) - 127 : 31 - __clz(m) - 149;
         const bool finite = m < 0x7F800000u;
-        const int sh = m == 0 || !finite ? 0 : 14 - lg;
+        const int sh = m == 0 ? 0 : 14 - lg;
         // 2^sh and 2^-sh may leave FP32's normal range: two factors
         const int sa = max(-100, min(100, sh));
         const float fa = pow2(sa), fb = pow2(sh - sa);
