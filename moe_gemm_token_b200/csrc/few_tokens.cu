@@ -900,14 +900,15 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS) few_kernel(const Args 
                 if (GROUPS == 1 || n <= LESS * SLOTS) run(std::integral_constant<int, LESS>());
                 else run(std::integral_constant<int, GROUPS>());
                 // the parts' sums, then the scales: of the rows, and of the columns' operand rows
+                // (last: the sum of a token near FP32's largest, shifted back, may not be an FP32 value yet)
 #pragma unroll
                 for (int q = 0; q < GROUPS; ++q) {
                     if constexpr (PT == 2) acc[q][0] += acc[q][1], acc[q][1] = acc[q][2] + acc[q][3];
 #pragma unroll
                     for (int j = 0; j < SUMS / 2; ++j) {
                         const float u = unshift[column(SLOTS * q + SUMS / 2 * t + j)];
-                        acc[q][j] = acc[q][j] * u * sr[0];
-                        acc[q][SUMS / 2 + j] = acc[q][SUMS / 2 + j] * u * sr[1];
+                        acc[q][j] = acc[q][j] * sr[0] * u;
+                        acc[q][SUMS / 2 + j] = acc[q][SUMS / 2 + j] * sr[1] * u;
                     }
                 }
             }

@@ -1,5 +1,5 @@
 """Values at the edges of the types in the few-token default-maths operators:
-infinities beside large finite values."""
+infinities beside large finite values, and tokens near the largest value."""
 import pytest
 import torch
 
@@ -72,3 +72,30 @@ def test_layer_of_tokens_with_an_infinity(metis, fmt, T, k):
     for row, sign in enumerate((INF, -INF, INF, -INF)):
         assert bool((y[row] == sign).all()), row
     assert torch.equal(y[4:], clean[4:])
+
+
+@by_format
+@pytest.mark.parametrize("T,k", [(2, 1), (5, 4), (60, 4)])
+def test_layer_of_very_large_tokens(metis, fmt, T, k):
+    """Tokens whose outputs are finite while the sums of codes alone, without the weights' scales, are not."""
+    d = few.layer(fmt, 1020 + T, T, 256, 256, 8, k)
+    d["x"] = (d["x"].float() * 2.0 ** 120).bfloat16()
+    y, bound = few.expect(fmt, d)
+    assert float(y.abs().max()) < 2.0 ** 127
+    got = few.run(metis, fmt, d)
+    assert metis.metis_check_device_status() == 0
+    ref.assert_within(got, y, bound)
+
+
+@pytest.mark.parametrize("M", [1, 3, 8])
+def test_streamed_product_of_very_large_tokens(metis, M):
+    N, K = 512, 1088
+    g = few.gen(1030 + M)
+    x = (torch.randn(M, K, generator=g, device="cuda") * 2.0 ** 120).bfloat16()
+    q, sf, gs = few.nvfp4_weights(g, 1, N, K)
+    y = torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    metis.metis_nvfp4_w4a16_gemm(x, q[0], sf, gs, y)
+    assert metis.metis_check_device_status() == 0
+    want, bound = ref.product(x, ref.nvfp4_values(q, sf, gs)[0])
+    assert float(want.abs().max()) < 2.0 ** 127
+    ref.assert_within(y, want, bound)
