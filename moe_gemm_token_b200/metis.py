@@ -8,7 +8,10 @@ runs in the library's CUDA kernels. There is no fallback: if the library is
 missing, :func:`load` raises.
 
 BF16 tensors may be ``torch.bfloat16`` or ``torch.int16``/``uint16`` bit
-patterns; E4M3 tensors ``torch.uint8`` or ``torch.float8_e4m3fn``.
+patterns; E4M3 tensors ``torch.uint8`` or ``torch.float8_e4m3fn``. The functions
+of the default maths for few tokens and of MXFP4 check types, shapes, devices
+and strides: BF16 is ``torch.bfloat16`` there, codes and scales are one-byte
+integers or the float type of that format.
 """
 import ctypes
 import os
@@ -47,6 +50,11 @@ MOE_WS = dict(COUNTS=0, OFFSETS=1, SLOT_TO_ROW=2, ROW_TO_SLOT=3, AQ=4, SA=5, H=6
 
 MOE4_WS = dict(COUNTS=0, OFFSETS=1, SLOT_TO_ROW=2, ROW_TO_SLOT=3, AQ=4, SFA=5, GA=6, H=7, HQ=8,
                SFH=9, GH=10, O=11)
+
+# What a tensor of one-byte codes may be declared as, by what the bytes are.
+_E4M3 = (torch.uint8, torch.float8_e4m3fn, torch.int8)
+_E2M1X2 = (torch.uint8, torch.float4_e2m1fn_x2, torch.int8)
+_E8M0 = (torch.uint8, torch.float8_e8m0fnu, torch.int8)
 
 _lib = None
 
@@ -355,7 +363,8 @@ def metis_moe_w8a16(x, topk_ids, topk_w, w_up, s_up, w_down, s_down, y, workspac
     for few tokens; see the C header for shapes."""
     name = "metis_moe_w8a16"
     if not (s_up.shape == w_up.shape[:2] and s_down.shape == w_down.shape[:2] and
-            s_up.dtype is torch.float32 and s_down.dtype is torch.float32 and w_up.element_size() == 1):
+            s_up.dtype is torch.float32 and s_down.dtype is torch.float32 and w_up.dtype in _E4M3 and
+            w_down.dtype in _E4M3):
         _refuse(name, "weights must be E4M3 bytes, s_up FP32 [E, I] and s_down FP32 [E, H]")
     return _moe_few(name, x, topk_ids, topk_w, (w_up, s_up), (w_down, s_down), 1, y, workspace, act, stream)
 
@@ -365,7 +374,8 @@ def metis_moe_nvfp4_w4a16(x, topk_ids, topk_w, w_up, sf_up, g_up, w_down, sf_dow
     """Routed-expert layer in the default maths with NVFP4 experts, for few
     tokens; weights and tiled scales as in :func:`metis_moe_nvfp4_grouped_gemm`."""
     name = "metis_moe_nvfp4_w4a16"
-    if not (sf_up.nbytes * 8 == w_up.nbytes and sf_down.nbytes * 8 == w_down.nbytes and w_up.element_size() == 1):
+    if not (sf_up.nbytes * 8 == w_up.nbytes and sf_down.nbytes * 8 == w_down.nbytes and w_up.dtype in _E2M1X2 and
+            w_down.dtype in _E2M1X2 and sf_up.dtype in _E4M3 and sf_down.dtype in _E4M3):
         _refuse(name, "weights must be packed bytes, sf_up and sf_down one byte per 16 elements")
     E = w_up.shape[0]
     if not (g_up.numel() == E == g_down.numel() and g_up.dtype is torch.float32 and g_down.dtype is torch.float32):
@@ -384,6 +394,8 @@ def metis_nvfp4_w4a16_gemm(x, qb, sfb, gb, y, workspace=None, stream=None):
         _refuse(name, "x and y must be torch.bfloat16")
     if not (qb.shape == (N, K // 2) and y.shape == (M, N) and sfb.nbytes * 16 >= (N + 127) // 128 * 128 * K):
         _refuse(name, "qb must be [N, K/2], sfb its tiled scales and y [M, N]")
+    if not (qb.dtype in _E2M1X2 and sfb.dtype in _E4M3):
+        _refuse(name, "qb must be packed bytes and sfb E4M3 bytes")
     if not (gb.numel() == 1 and gb.dtype is torch.float32):
         _refuse(name, "gb must be one FP32 value")
     device = torch.cuda.current_device()
@@ -409,6 +421,8 @@ def metis_quant_mxfp4(x, q, sf, tiled=False, stream=None):
     rows = (R + 127) // 128 * 128 if tiled else R
     if q.nbytes * 2 < R * K or sf.nbytes * 32 < rows * K:
         _refuse(name, "q or sf is too small")
+    if not (q.dtype in _E2M1X2 and sf.dtype in _E8M0):
+        _refuse(name, "q must be packed bytes and sf E8M0 bytes")
     device = torch.cuda.current_device()
     pq, ps = _pointers(name, device, (q, sf))
     if x.get_device() != device:
@@ -427,6 +441,8 @@ def metis_dequant_mxfp4(q, sf, y, tiled=False, stream=None):
         _refuse(name, "y must be torch.bfloat16")
     if q.nbytes * 2 < R * K or sf.nbytes * 32 < rows * K:
         _refuse(name, "q or sf is too small")
+    if not (q.dtype in _E2M1X2 and sf.dtype in _E8M0):
+        _refuse(name, "q must be packed bytes and sf E8M0 bytes")
     device = torch.cuda.current_device()
     pq, ps, py = _pointers(name, device, (q, sf, y))
     return _check(name, (_lib or load()).metis_dequant_mxfp4(
@@ -446,6 +462,8 @@ def metis_mxfp4_gemm(qa, sfa, qb, sfb, y, stream=None):
         _refuse(name, "qa must be [ceil(M/128) * 128, K/2] and qb [N, K/2]")
     if sfa.nbytes * 16 < rows * kb or sfb.nbytes * 16 < (N + 127) // 128 * 128 * kb:
         _refuse(name, "sfa or sfb is too small")
+    if not (qa.dtype in _E2M1X2 and qb.dtype in _E2M1X2 and sfa.dtype in _E8M0 and sfb.dtype in _E8M0):
+        _refuse(name, "qa and qb must be packed bytes, sfa and sfb E8M0 bytes")
     device = torch.cuda.current_device()
     pa, psa, pb, psb, py = _pointers(name, device, (qa, sfa, qb, sfb, y))
     return _check(name, (_lib or load()).metis_mxfp4_gemm(pa, psa, pb, psb, py, M, N, 2 * kb, _stream(device, stream)))
