@@ -291,6 +291,13 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
 
 // ------------------------------------------------------------- tcgen05/TMEM
 
+// Shared memory that every kernel which allocates TMEM takes at least: more
+// than half of an SM's 228 KB (1 KB per CTA is the system's), so that no SM
+// holds two of them. Each takes all 512 columns and keeps them while it waits
+// for the other CTAs of its cluster; two such CTAs on one SM could make two
+// clusters wait for one another.
+constexpr size_t TMEM_CTA_SMEM = 114 * 1024;
+
 __device__ __forceinline__ void tmem_alloc(uint32_t slot_smem, uint32_t ncols) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      slot_smem),

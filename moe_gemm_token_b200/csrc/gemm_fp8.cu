@@ -98,6 +98,7 @@ struct Layout {
     static constexpr int GROUP_OFF = MISC_OFF + 16;
     static constexpr size_t BYTES_DENSE = 1024 + GROUP_OFF;
     static constexpr size_t BYTES_GROUPED = BYTES_DENSE + 2 * (MAX_GROUPS + 1) * 4;
+    static_assert(BYTES_DENSE >= TMEM_CTA_SMEM, "one CTA with TMEM per SM");
     static constexpr uint32_t IDESC = W16 ? idesc_bf16_f32(ROWS * CTAS, BN) : idesc_e4m3_f32(ROWS * CTAS, BN);
     static constexpr int KE = W16 ? BK / 2 : BK;  // elements per k-block row
 };

@@ -544,6 +544,7 @@ struct Lay {
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
     static constexpr int GROUP_OFF = MISC_OFF + 16;
     static constexpr size_t BYTES = 1024 + GROUP_OFF + (GROUPED ? 3 * (MAX_GROUPS + 1) * 4 : 0);
+    static_assert(BYTES >= TMEM_CTA_SMEM, "one CTA with TMEM per SM");
     // chunk c of a k-block
     static constexpr uint32_t idesc(int c) {
         return MX ? idesc_mxf4(ROWS * CTAS, BN, c & 1) : idesc_nvf4(ROWS * CTAS, BN);

@@ -79,7 +79,9 @@ struct Cfg {
     // full[S] (x bytes + converter arrivals), empty[S], tfull[ACCS], tempty[ACCS], drain
     static constexpr int NUM_BARS = 2 * STAGES + 2 * ACCS + 1;
     static constexpr int MISC_OFF = BAR_OFF + NUM_BARS * 8;
-    static constexpr size_t SMEM_BYTES = 1024 + MISC_OFF + 16;
+    // (the ring of 32 or 64 tokens would leave room for a second CTA)
+    static constexpr size_t USED = 1024 + MISC_OFF + 16;
+    static constexpr size_t SMEM_BYTES = USED > TMEM_CTA_SMEM ? USED : TMEM_CTA_SMEM;
     static_assert(TM == 32 || TM == 64 || TM == 128 || TM == 256, "tile width");
     static_assert(A_COL0 + STAGES * A_COLS <= TMEM_COLS, "TMEM budget");
 };
@@ -545,7 +547,8 @@ int launch_w8a16_tensor(const __nv_bfloat16* x, const uint8_t* wq, const float* 
 
 namespace w16 {
 
-// Clusters of so many CTAs of the split kernel that are resident at once (one CTA per SM for every TM).
+// Clusters of so many CTAs of the split kernel that are resident at once (one
+// CTA per SM for every TM: TMEM_CTA_SMEM).
 std::atomic<int> resident[64][MAX_KS + 1];
 
 int prepare_fp4(const DeviceInfo& di) {
