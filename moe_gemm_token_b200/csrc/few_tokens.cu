@@ -1095,13 +1095,35 @@ int check_moe(const char* name, int act, int64_t T, int64_t topk, int64_t E, int
     return METIS_OK;
 }
 
-// Launches few_kernel, one CTA per SM, with as many staged operand rows as are
-// of use (OWN: all slots; else the columns of two jobs) and fit: for 8 warps in
-// half of the shared memory if that holds a job's rows, so that the next
-// kernel's CTAs find room, else in all of it.
+// The shared memory of few_kernel with P staged operand rows (a.pitch is set).
+template <int FMT, int MODE, int GMAX, int W>
+int few_bytes(const Args& a, int P) {
+    return smem_layout<FMT, MODE, GMAX, W>(Geo<FMT>::SLOT, P, a.pitch, a.E, a.S).total;
+}
+
+// Sets the operand's layout: as many staged rows P as are of use (OWN: all
+// slots; by_token: all tokens; else the slots of two jobs) and fit: for 8 warps
+// in half of the shared memory if that holds a job's rows, so that the next
+// kernel's CTAs find room, else in all of it. False: not even one does, or not
+// all where all are needed.
+template <int FMT, int MODE, int GMAX, int W>
+bool stage_plan(const DeviceInfo& di, Args& a) {
+    a.pitch = operand_pitch<FMT>(a.w.K);
+    const int base = few_bytes<FMT, MODE, GMAX, W>(a, 0) + 32;  // rounding
+    const int row = PARTS<MODE> * a.pitch + 8;
+    const int half = (112 * 1024 - base) / row, full = (di.max_smem_optin - base) / row;
+    const int per_job = a.T < 8 * GMAX ? a.T : 8 * GMAX;
+    // a few tokens that all threads read with one round trip
+    a.by_token = MODE == UP && a.T <= W && static_cast<int64_t>(a.T) * a.w.K <= 8 * STAGE_U * 32 * W;
+    const int want = a.by_token ? a.T : MODE == OWN || a.S < 2 * per_job ? a.S : 2 * per_job;
+    const int room = W == 8 && half >= (MODE == OWN ? want : per_job) ? half : full;
+    a.P = want < room ? want : room;
+    return a.P >= 1 && (a.P >= want || !(MODE == OWN || a.by_token));
+}
+
+// Launches few_kernel, one CTA per SM.
 template <int FMT, int MODE, int GMAX, int W>
 int launch_few(const DeviceInfo& di, Args a, cudaStream_t st) {
-    using G = Geo<FMT>;
     static std::atomic<uint64_t> done[64];
     int rc = once_per_context(done, di.device, [&] {
         const auto f = few_kernel<FMT, MODE, GMAX, W>;
@@ -1116,22 +1138,11 @@ int launch_few(const DeviceInfo& di, Args a, cudaStream_t st) {
         return r;
     });
     if (rc) return rc;
-    a.pitch = operand_pitch<FMT>(a.w.K);
-    auto bytes = [&](int P) { return smem_layout<FMT, MODE, GMAX, W>(G::SLOT, P, a.pitch, a.E, a.S).total; };
-    const int base = bytes(0) + 32;  // rounding
-    const int row = PARTS<MODE> * a.pitch + 8;
-    const int half = (112 * 1024 - base) / row, full = (di.max_smem_optin - base) / row;
-    const int per_job = a.T < 8 * GMAX ? a.T : 8 * GMAX;
-    // a few tokens that all threads read with one round trip
-    a.by_token = MODE == UP && a.T <= W && static_cast<int64_t>(a.T) * a.w.K <= 8 * STAGE_U * 32 * W;
-    const int want = a.by_token ? a.T : MODE == OWN || a.S < 2 * per_job ? a.S : 2 * per_job;
-    const int room = W == 8 && half >= (MODE == OWN ? want : per_job) ? half : full;
-    a.P = want < room ? want : room;
-    if (a.P < 1 || ((MODE == OWN || a.by_token) && a.P < want))
+    if (!stage_plan<FMT, MODE, GMAX, W>(di, a))
         return fail(METIS_ERR_UNSUPPORTED, "few-token kernel: K=%d is too long", a.w.K);
     a.grid_inv = 0xFFFFFFFFu / static_cast<uint32_t>(di.num_sms);
     a.tiles_inv = 0xFFFFFFFFu / static_cast<uint32_t>((a.w.N + 15) / 16);
-    return cuda_check(launch_pdl(few_kernel<FMT, MODE, GMAX, W>, dim3(di.num_sms), dim3(W * 32), bytes(a.P), st, 1, a),
+    return cuda_check(launch_pdl(few_kernel<FMT, MODE, GMAX, W>, dim3(di.num_sms), dim3(W * 32), few_bytes<FMT, MODE, GMAX, W>(a, a.P), st, 1, a),
                       "few-token kernel launch");
 }
 
@@ -1141,13 +1152,30 @@ int launch_few(const DeviceInfo& di, Args a, cudaStream_t st) {
 // rows of an operand in one part, 6 (FP8) or 8 (NVFP4) in two (20 tokens top-4
 // on 16 experts 1024 x 4096, the down-projection with 8 and 16 warps: FP8 48.9,
 // 41.6; NVFP4 44.3, 39.9).
-template <int FMT, int MODE>
-int launch_few_by_size(const DeviceInfo& di, const Args& a, int columns, int64_t weight_bytes, cudaStream_t st) {
+// Calls go(GMAX, W).
+template <int FMT, int MODE, typename F>
+auto by_size(const DeviceInfo& di, const Args& a, int columns, int64_t weight_bytes, F&& go) {
+    using std::integral_constant;
     const bool small = weight_bytes < di.num_sms * 160ll * 1024;
     const bool long_rows = PARTS<MODE> * operand_pitch<FMT>(a.w.K) * 8 > (PARTS<MODE> == 2 ? 140 : 112) * 1024;
-    if ((columns <= 8 && small) || long_rows) return launch_few<FMT, MODE, 1, 8>(di, a, st);
-    if (columns <= 8) return launch_few<FMT, MODE, 1, 16>(di, a, st);
-    return launch_few<FMT, MODE, 2, 16>(di, a, st);
+    if ((columns <= 8 && small) || long_rows) return go(integral_constant<int, 1>(), integral_constant<int, 8>());
+    if (columns <= 8) return go(integral_constant<int, 1>(), integral_constant<int, 16>());
+    return go(integral_constant<int, 2>(), integral_constant<int, 16>());
+}
+template <int FMT, int MODE>
+int launch_few_by_size(const DeviceInfo& di, const Args& a, int columns, int64_t weight_bytes, cudaStream_t st) {
+    return by_size<FMT, MODE>(di, a, columns, weight_bytes,
+                              [&](auto g, auto w) { return launch_few<FMT, MODE, decltype(g)::value, decltype(w)::value>(di, a, st); });
+}
+
+// DENSE: tokens of a job (with fewer than all, every job streams and widens all weights); 0: none can be staged.
+inline int job_tokens(const DeviceInfo& di, Args a, int64_t weight_bytes) {
+    return by_size<NVFP4, DENSE>(di, a, a.S, weight_bytes, [&](auto g, auto w) {
+        constexpr int columns = 8 * decltype(g)::value;
+        if (!stage_plan<NVFP4, DENSE, decltype(g)::value, decltype(w)::value>(di, a)) return 0;
+        const int most = a.P < columns ? a.P : columns;
+        return a.S < most ? a.S : most;
+    });
 }
 
 template <int FMT>
@@ -1219,12 +1247,17 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
 constexpr int64_t kStreamTokens = 16, kWidenTokens = 3000;
 
 // Up to kStreamTokens, by estimates fitted to the table, in ns: 3000 + 100 per
-// 1024 staged operand values + the codes at 3.2 TB/s + 500 for a second group
-// of columns, against 3750 + 530 per stage. The stream's operand has to fit
-// shared memory in one piece.
-static bool nvfp4_w4a16_streams(int64_t M, int64_t N, int64_t K, const W4a16Plan& plan) {
-    return M <= kStreamTokens && (M == 1 || (M <= 8 ? M : 8) * K <= 80 * 1024) &&
-           M * K * 100 / 1024 + N * K / 6400 + (M > 8 ? 500 : 0) < 750 + 530 * plan.stages;
+// 1024 operand values that a CTA stages (a job's) + the codes at 3.2 TB/s, once
+// for every job (long rows: fewer tokens fit shared memory) + 500 for a second
+// group of columns, against 3750 + 530 per stage. Two jobs, us, streamed and
+// tensor cores: 16 x 14336 x 4352 26.9, 22.0; 13 x 12288 x 5632 31.7, 27.3; 9 x
+// 14336 x 7104 37.8, 35.6; 16 x 9600 x 5120 25.1, 24.9; 16 x 9600 x 8192 31.2,
+// 37.5; 9 x 9600 x 8192 32.2, 37.5; 6 x 9600 x 13632 50.5, 63.6.
+static bool nvfp4_w4a16_streams(const DeviceInfo& di, const few::Args& a, const W4a16Plan& plan) {
+    const int64_t M = a.S, N = a.w.N, K = a.w.K;
+    if (M > kStreamTokens) return false;
+    const int64_t job = few::job_tokens(di, a, N * K / 2);
+    return job > 0 && job * K * 100 / 1024 + (M + job - 1) / job * (N * K / 6400) + (job > 8 ? 500 : 0) < 750 + 530 * plan.stages;
 }
 
 size_t nvfp4_w4a16_workspace(int64_t M, int64_t N, int64_t K) {
@@ -1315,10 +1348,17 @@ extern "C" int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, con
     int rc = current_device_info(&di);
     if (rc) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
+    few::Args a{};
+    a.in = x_bf16;
+    a.w = few::Weights{qb, sfb, gb, static_cast<int>(N), static_cast<int>(K)};
+    a.E = 1;
+    a.S = a.T = static_cast<int>(M);
+    a.topk = 1;
+    a.out = y_bf16;
     if (M <= kWidenTokens) {
         W4a16Plan plan;
         if ((rc = plan_nvfp4_w4a16_tensor(static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), &plan))) return rc;
-        if (!nvfp4_w4a16_streams(M, N, K, plan))
+        if (!nvfp4_w4a16_streams(di, a, plan))
             return launch_nvfp4_w4a16_tensor(plan, static_cast<const __nv_bfloat16*>(x_bf16), qb, sfb, gb,
                                              static_cast<__nv_bfloat16*>(y_bf16), static_cast<int>(M), static_cast<int>(N),
                                              static_cast<int>(K), st);
@@ -1341,13 +1381,6 @@ extern "C" int metis_nvfp4_w4a16_gemm(const void* x_bf16, const uint8_t* qb, con
         return launch_bf16_gemm(static_cast<const __nv_bfloat16*>(x_bf16), wide, static_cast<__nv_bfloat16*>(y_bf16),
                                 static_cast<int>(M), static_cast<int>(N), static_cast<int>(K), col, st);
     }
-    few::Args a{};
     if ((rc = device_status_word(&a.status))) return rc;
-    a.in = x_bf16;
-    a.w = few::Weights{qb, sfb, gb, static_cast<int>(N), static_cast<int>(K)};
-    a.E = 1;
-    a.S = a.T = static_cast<int>(M);
-    a.topk = 1;
-    a.out = y_bf16;
     return few::launch_few_by_size<few::NVFP4, few::DENSE>(di, a, a.S, N * K / 2, st);
 }
