@@ -12,9 +12,10 @@
 //  * few_kernel, one launch per projection. Each CTA builds the routing from
 //    the ids itself: jobs (an expert with up to 8 or 16 of its slots), whose
 //    16-row tiles are shared out evenly over the CTAs. A warp streams its
-//    tiles' weights through lane-private places of shared memory (cp.async,
-//    64 KB and more in flight per SM, any row granularity: per-row bulk copies
-//    were bound by their issue, 46 per microsecond and CTA), widens them to
+//    tiles' weights through lane-private places of shared memory (cp.async, any
+//    row granularity: per-row bulk copies were bound by their issue, 46 per
+//    microsecond and CTA; in flight per CTA, FP8 64 KB with 8 warps and 96 with
+//    16, NVFP4 48 and 64 KB of codes), widens them to
 //    FP16 (E4M3, and E2M1 times an E4M3 block scale, are exact FP16 values)
 //    and multiplies with mma.sync m16n8k16, the weights as the 16 rows and the
 //    job's tokens as the 8 columns. A tile's K is split over ks warps when
@@ -1244,6 +1245,8 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
 //        widened first       63.0                    79 - 85     14.8
 //  4096  tensor cores        90.9                    80          14.2
 //        widened first       82.5                    84          17.8
+// The border by tokens alone is right for the wide matrix; the two small ones
+// would still be 5 and 20% faster without the widening at 4096 tokens.
 constexpr int64_t kStreamTokens = 16, kWidenTokens = 3000;
 
 // Up to kStreamTokens, by estimates fitted to the table, in ns: 3000 + 100 per

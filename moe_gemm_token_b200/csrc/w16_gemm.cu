@@ -7,13 +7,13 @@
 // the only thing rounded).
 //
 // Computed as y^T = W x^T so that the widened weights never pass through
-// shared memory: a 128-channel x TM-token tile per CTA (TM = 128 or 256),
-// the channels on the 128 TMEM lanes.
+// shared memory: a 128-channel x TM-token tile per CTA (TM = 128 or 256; NVFP4
+// weights also 32 or 64), the channels on the 128 TMEM lanes.
 //   warp 0      TMA producer of the x tiles (BF16, TM tokens x 128 elements
 //               as two 64-element boxes, 128-byte swizzle) into a
-//               shared-memory ring (4 stages for TM = 128, 3 for 256);
+//               shared-memory ring (4 stages up to TM = 128, 3 for 256);
 //   warp 1      allocates all 512 TMEM columns (FP32 accumulators: two of
-//               128 columns, or one of 256; 64-column weight stages after
+//               TM columns, or one of 256; 64-column weight stages after
 //               them); one lane issues tcgen05.mma.kind::f16 with A = the
 //               widened weights in TMEM and B = the x tile in shared memory,
 //               8 MMAs (K = 16) per stage;
@@ -60,7 +60,7 @@ template <bool FP4>
 constexpr int pf() { return FP4 ? 2 : 4; }
 constexpr int THREADS = 64 + CONV_WARPS * 32 + 4 * 32;
 
-// Tiles of TM tokens (accumulator columns). TM = 128: two accumulators (the
+// Tiles of TM tokens (accumulator columns). TM up to 128: two accumulators (the
 // epilogue drains one while the MMAs fill the other) and 4 weight stages.
 // TM = 256: N = 256 MMAs, half as many per FLOP for the one issuing thread;
 // TMEM then holds one accumulator and 3 weight stages, so the epilogue's
@@ -69,7 +69,7 @@ template <int TM>
 struct Cfg {
     static constexpr int ACCS = TM <= 128 ? 2 : 1;
     static constexpr int STAGES = TM <= 128 ? 4 : 3;  // x ring and TMEM weight stages
-    static constexpr int X_BOX = TM * BOXE * 2;       // 16 or 32 KB
+    static constexpr int X_BOX = TM * BOXE * 2;       // 4 (TM = 32) to 32 KB
     static constexpr int X_STAGE = 2 * X_BOX;
     static constexpr int A_COL0 = ACCS * TM;          // weight stages after the accumulators
     static constexpr uint32_t IDESC = idesc_bf16_f32(TILE_N, TM);
@@ -87,7 +87,7 @@ struct Cfg {
 };
 
 struct Params {
-    const uint8_t* w;     // [N, K] E4M3
+    const uint8_t* w;     // [N, K] E4M3; FP4: [N, K / 2] packed codes
     const float* s_w;     // [N]; FP4: the one global scale
     const uint8_t* sf;    // FP4: tiled block scales
     __nv_bfloat16* y;     // [M, N]
