@@ -208,6 +208,12 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
+// Two FP32 values -> FP16, nearest even, infinities the largest finite value.
+__device__ __forceinline__ uint32_t f16x2_saturated(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
 // The two E4M3 scales in the low half of w, each as an FP16 pair of itself.
 __device__ __forceinline__ void scale_pairs(uint32_t w, uint32_t& s0, uint32_t& s1) {
     uint32_t h;
@@ -231,9 +237,10 @@ __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cas
 // within 2^-29 of the largest; FP32 values with PARTS = 2 lose less than 2^-22
 // of theirs or 2^-39 of the largest). A row with an infinity or a NaN is
 // shifted as if its largest were 2^128, so that its finite values stay finite
-// (what they add to a sum with an infinity does not matter), and its second
-// parts are zeros. 16-byte chunks are stored in the order in which the lanes
-// read them (operand_chunk), zeros from K to the end of the last piece.
+// (what they add to a sum with an infinity does not matter); with two parts the
+// first is the largest FP16 value and the second the infinity. 16-byte chunks
+// are stored in the order in which the lanes read them (operand_chunk), zeros
+// from K to the end of the last piece.
 template <int FMT>
 __device__ __forceinline__ int operand_chunk(int q) {
     constexpr int C = Geo<FMT>::CH;  // a half's chunk t * C + i is stored at i * 4 + t
@@ -366,7 +373,6 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
         m = __reduce_max_sync(0xffffffffu, m);
         // floor(log2(m)) = bits' exponent - 127 (not finite: 128); a subnormal m has its leading bit at 31 - clz
         const int lg = m >= 0x00800000u ? static_cast<int>(m >> 23) - 127 : 31 - __clz(m) - 149;
-        const bool finite = m < 0x7F800000u;
         const int sh = m == 0 ? 0 : 14 - lg;
         // 2^sh and 2^-sh may leave FP32's normal range: two factors
         const int sa = max(-100, min(100, sh));
@@ -391,12 +397,15 @@ __device__ __forceinline__ void stage_rows(int n, int K, uint8_t* dst, int pitch
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float lo = j ? f[2 * k] : f[2 * k] * fa, hi = j ? f[2 * k + 1] : f[2 * k + 1] * fa;
-                        const __half2 p = __floats2half2_rn(lo, hi);
-                        h[k] = *reinterpret_cast<const uint32_t*>(&p);
-                        if (j + 1 < PARTS) {  // what the rounding left, exactly
-                            const float2 r = __half22float2(p);
-                            f[2 * k] = finite ? lo - r.x : 0.0f;
-                            f[2 * k + 1] = finite ? hi - r.y : 0.0f;
+                        if (j + 1 < PARTS) {
+                            h[k] = f16x2_saturated(lo, hi);
+                            // what the rounding left, exactly
+                            const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&h[k]));
+                            f[2 * k] = lo - r.x;
+                            f[2 * k + 1] = hi - r.y;
+                        } else {
+                            const __half2 p = __floats2half2_rn(lo, hi);
+                            h[k] = *reinterpret_cast<const uint32_t*>(&p);
                         }
                     }
                     // past K: zeros (a second batch there is not what the lane kept)
@@ -1210,13 +1219,12 @@ int run_moe(const DeviceInfo& di, const __nv_bfloat16* x, const int32_t* ids, co
     a.in = h;
     a.w = down;
     // few slots: every CTA stages all of h and owns rows of the output, which
-    // saves the last launch; against DOWN, us a call: 8 slots 2048 x 1024 12.6,
-    // 14.2; 8 slots 512 x 256 7.7, 8.5. With more slots only where the CTA's rows
-    // nearly fill its tiles of 16: 16 slots 2048 x 1024 19.2, 20.0, but 16 slots
-    // 1024 x 512 11.0, 10.5; 24 slots 15.3, 12.2.
-    const int rows = (down.N + di.num_sms - 1) / di.num_sms;
-    const bool filled = 5 * rows >= 4 * 16 * ((rows + 15) / 16);
-    if ((S <= 8 || (S <= 16 && filled)) && PARTS<OWN> * S * operand_pitch<FMT>(down.K) <= 80 * 1024) {
+    // saves a launch. Against DOWN, us a call in a graph (FP8): 8 slots 2048 x 1024
+    // 12.6, 14.2, 512 x 256 7.7, 8.5; 16 slots 2048 x 1024 19.3, 20.1, 2048 x 512
+    // 13.3, 14.2, but 1024 x 512 11.2, 10.3 and 15 slots 1040 x 528 13.5, 11.7,
+    // which calls from the host turn round (12.7, 15.0 and 14.0, 15.1); 24 slots
+    // 1024 x 512 14.2, 12.2, 48 slots 512 x 256 17.2, 11.2.
+    if (S <= 16 && PARTS<OWN> * S * operand_pitch<FMT>(down.K) <= 80 * 1024) {
         a.out = y;
         return launch_few<FMT, OWN, 1, 8>(di, a, st);
     }
